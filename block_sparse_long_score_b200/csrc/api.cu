@@ -484,7 +484,8 @@ int xattn_get_device_status(void* stream) {
       return XATTN_ERR_CUDA;
   }
   if (v == kStatusTimeout) return XATTN_ERR_TIMEOUT;
-  if (v == kStatusBadTau) return XATTN_ERR_INVALID_ARG;
+  if (v == kStatusBadTau || v == kStatusBadCache) return XATTN_ERR_INVALID_ARG;
+  if (v == kStatusNoPages) return XATTN_ERR_PAGES;
   return XATTN_OK;
 }
 
@@ -496,6 +497,7 @@ const char* xattn_strerror(int status) {
     case XATTN_ERR_CUDA: return "CUDA runtime error";
     case XATTN_ERR_WORKSPACE: return "workspace missing or too small";
     case XATTN_ERR_TIMEOUT: return "a kernel wait timed out";
+    case XATTN_ERR_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

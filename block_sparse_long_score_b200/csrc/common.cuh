@@ -14,6 +14,8 @@ namespace xattn {
 // Device status codes written into the per-device status word.
 constexpr int kStatusTimeout = 1;
 constexpr int kStatusBadTau = 2;  // a device-resident tau was outside (0, 1] (or NaN)
+constexpr int kStatusBadCache = 3;  // a length, page or slot of a paged cache was out of range
+constexpr int kStatusNoPages = 4;   // a plan needed more pages than were free
 
 struct Dims {
   int batch, hq, hkv, L, d, B, S, causal, dtype;

@@ -24,7 +24,8 @@ __all__ = [
     "antidiagonal_perm", "diagonal_perm", "xattn_score_select", "xattn_selftest_timeout",
     "xattn_prefill_host_workspace_bytes", "xattn_prefill_host",
     "xattn_prefill_varlen_workspace_bytes", "xattn_prefill_varlen", "xattn_check_lists",
-    "xattn_score_partials",
+    "xattn_score_partials", "xattn_paged_plan", "xattn_paged_append", "xattn_paged_decode",
+    "xattn_paged_decode_workspace_bytes", "make_paged",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +39,8 @@ EXPORTED_SYMBOLS = (
     "xattn_select_topk", "xattn_select_topratio", "xattn_score_select",
     "xattn_selftest_timeout", "xattn_prefill_host_workspace_bytes", "xattn_prefill_host",
     "xattn_prefill_varlen_workspace_bytes", "xattn_prefill_varlen", "xattn_check_lists",
-    "xattn_score_partials",
+    "xattn_score_partials", "xattn_paged_plan", "xattn_paged_append", "xattn_paged_decode",
+    "xattn_paged_decode_workspace_bytes",
 )
 # batch * hq * NB limit of xattn_sparse_attn_noalloc (XATTN_NOALLOC_MAX_UNITS)
 NOALLOC_MAX_UNITS = 1 << 18
@@ -53,6 +55,12 @@ class XattnError(RuntimeError):
 class _Shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in
                 ("batch", "hq", "hkv", "L", "d", "B", "S", "causal", "dtype")]
+
+
+class _Paged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in
+                ("nseq", "max_pages", "num_pages", "page_size", "hq", "hkv", "d", "dtype")] + \
+               [(n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "token_stride")]
 
 
 _lib_handle = None
@@ -110,6 +118,15 @@ def _lib() -> ctypes.CDLL:
         lib.xattn_prefill_varlen.restype = i32
         lib.xattn_check_lists.argtypes = [vp, vp, sp, vp, vp]
         lib.xattn_check_lists.restype = i32
+        pp, i64 = ctypes.POINTER(_Paged), ctypes.c_longlong
+        lib.xattn_paged_plan.argtypes = [i32] * 5 + [vp] * 10
+        lib.xattn_paged_plan.restype = i32
+        lib.xattn_paged_append.argtypes = [vp, vp, pp, i32, i32, i64, vp, vp, vp, vp, vp]
+        lib.xattn_paged_append.restype = i32
+        lib.xattn_paged_decode_workspace_bytes.argtypes = [pp]
+        lib.xattn_paged_decode_workspace_bytes.restype = sz
+        lib.xattn_paged_decode.argtypes = [vp, vp, vp, pp, vp, vp, vp, vp, vp, sz, vp]
+        lib.xattn_paged_decode.restype = i32
         lib.xattn_selftest_timeout.argtypes = [vp]
         lib.xattn_selftest_timeout.restype = i32
         lib.xattn_get_device_status.argtypes = [vp]
@@ -613,6 +630,192 @@ def xattn_prefill_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
                                          workspace.numel() * workspace.element_size(),
                                          _stream(Q.device))
     _raise("xattn_prefill_varlen", rc)
+    return (out, lse) if want_lse else out
+
+
+XATTN_TOKEN_MAJOR, XATTN_HEAD_MAJOR = 0, 1
+
+
+def make_paged(k_pages: torch.Tensor, hq: int, nseq: int, max_pages: int) -> _Paged:
+    """Shape of a paged cache whose pages are ``k_pages`` [num_pages, hkv,
+    page_size, d] (any strides with contiguous features)."""
+    if k_pages.dim() != 4:
+        raise ValueError("pages must be [num_pages, hkv, page_size, d]")
+    num_pages, hkv, page, d = k_pages.shape
+    if k_pages.dtype == torch.bfloat16:
+        dt = XATTN_BF16
+    elif k_pages.dtype == torch.float32:
+        dt = XATTN_F32
+    else:
+        raise ValueError(f"pages must be bfloat16 or float32, got {k_pages.dtype}")
+    ps, hs, ts, es = k_pages.stride()
+    if es != 1:
+        raise ValueError("the features of a page's row must be contiguous")
+    # the stride of an axis of one entry is never used
+    return _Paged(nseq, max_pages, num_pages, page, hq, hkv, d, dt, ps if num_pages > 1 else d,
+                  hs if hkv > 1 else d, ts)
+
+
+def _paged_pair(k_pages, v_pages, hq: int, nseq: int, max_pages: int) -> _Paged:
+    """Shape of the cache, after checking the V pages against the K pages."""
+    if not (k_pages.is_cuda and v_pages.is_cuda):
+        raise ValueError("the pages must be CUDA tensors")
+    if v_pages.dtype != k_pages.dtype or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same type and shape")
+    shape = make_paged(k_pages, hq, nseq, max_pages)
+    if v_pages.stride() != k_pages.stride():
+        other = make_paged(v_pages, hq, nseq, max_pages)
+        if (other.page_stride, other.head_stride, other.token_stride) != \
+                (shape.page_stride, shape.head_stride, shape.token_stride):
+            raise ValueError("k_pages and v_pages must have the same strides")
+    return shape
+
+
+def xattn_paged_plan(lens: torch.Tensor, fresh: torch.Tensor, pool: torch.Tensor,
+                     ring: torch.Tensor, table: torch.Tensor, page_size: int,
+                     max_tokens: Optional[int] = None, out: Optional[tuple] = None):
+    """One step's block table and slot map, built on the device (see
+    include/xattn.h): ``fresh[i]`` new tokens for request i, -1 where it ends.
+    All tensors int32: lens, fresh [nseq], pool [2], ring [num_pages], table
+    [nseq, max_pages]; ``table`` and ``ring`` are updated in place. ``out`` is
+    (lens, pool, starts [nseq + 1], slots [max_tokens]) to write to (the first
+    two may be the inputs themselves); without it they are allocated, with
+    room for ``max_tokens`` slots. Returns (lens, pool, starts, slots)."""
+    for t, n in ((lens, "lens"), (fresh, "fresh"), (pool, "pool"), (ring, "ring"),
+                 (table, "table")):
+        _check(t, n, torch.int32)
+    if lens.dim() != 1 or table.dim() != 2 or ring.dim() != 1:
+        raise ValueError("expected lens [nseq], ring [num_pages] and table [nseq, max_pages]")
+    nseq = lens.shape[0]
+    if table.shape[0] != nseq:
+        raise ValueError("table needs a row for each request")
+    _check_shape(fresh, (nseq,), "fresh")
+    _check_shape(pool, (2,), "pool")
+    if out is None:
+        if max_tokens is None:
+            raise ValueError("max_tokens is needed when no buffers are given")
+        out = (torch.empty_like(lens), torch.empty_like(pool),
+               torch.empty(nseq + 1, device=lens.device, dtype=torch.int32),
+               torch.empty(max_tokens, device=lens.device, dtype=torch.int32))
+    lens_out, pool_out, starts, slots = out
+    for t, n in ((lens_out, "lens output"), (pool_out, "pool output"), (starts, "starts"),
+                 (slots, "slots")):
+        _check(t, n, torch.int32)
+    _check_shape(lens_out, (nseq,), "lens output")
+    _check_shape(pool_out, (2,), "pool output")
+    _check_shape(starts, (nseq + 1,), "starts")
+    if slots.dim() != 1 or (max_tokens is not None and slots.shape[0] != max_tokens):
+        raise ValueError("slots must be [max_tokens]")
+    _same_device(lens, fresh, pool, ring, table, lens_out, pool_out, starts, slots)
+    with torch.cuda.device(lens.device):
+        rc = _lib().xattn_paged_plan(
+            nseq, page_size, ring.shape[0], table.shape[1], slots.shape[0], lens.data_ptr(),
+            fresh.data_ptr(), pool.data_ptr(), ring.data_ptr(), table.data_ptr(),
+            lens_out.data_ptr(), pool_out.data_ptr(), starts.data_ptr(), slots.data_ptr(),
+            _stream(lens.device))
+    _raise("xattn_paged_plan", rc)
+    return out
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the tokens of a [tokens, hkv, d] tensor whose tokens
+    are contiguous themselves (a slice of a fused projection is one)."""
+    n, hkv, d = t.shape
+    if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d):
+        raise ValueError(f"the [hkv, d] rows of {name} must be contiguous")
+    return t.stride(0) if n > 1 else hkv * d
+
+
+def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
+                       k_pages: torch.Tensor, v_pages: torch.Tensor,
+                       starts: Optional[torch.Tensor] = None) -> None:
+    """Writes the keys and values of new tokens to their slots (-1: left out).
+
+    Without ``starts``, K and V are [tokens, hkv, d], one row per slot. With
+    ``starts`` (int32 [nseq + 1]), they are request after request, each a
+    contiguous [hkv, L_i, d] array: the packed layout of xattn_prefill_varlen,
+    or [batch, hkv, L, d] tensors; they hold len(slots) tokens' rows."""
+    _check(slots, "slots", torch.int32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [tokens]")
+    if K.dtype != k_pages.dtype or V.dtype != k_pages.dtype:
+        raise ValueError("K, V and the pages must have one type")
+    tokens, nseq = slots.shape[0], 1
+    if starts is None:
+        if K.dim() != 3 or K.shape != (tokens,) + (k_pages.shape[1], k_pages.shape[3]) \
+                or V.shape != K.shape:
+            raise ValueError("without starts, K and V must be [len(slots), hkv, d]")
+        stride = _token_stride(K, "K")
+        if _token_stride(V, "V") != stride:
+            raise ValueError("K and V must have the same token stride")
+    else:
+        _check(K, "K")
+        _check(V, "V")
+        _check(starts, "starts", torch.int32)
+        nseq, stride = starts.numel() - 1, 0
+        rows = tokens * k_pages.shape[1] * k_pages.shape[3]
+        if nseq < 1 or K.numel() != rows or V.numel() != rows:
+            raise ValueError("with starts, K and V must hold len(slots) * hkv rows of d")
+    shape = _paged_pair(k_pages, v_pages, 1, nseq, 1)
+    _same_device(k_pages, K, V, slots, starts, v_pages)
+    with torch.cuda.device(k_pages.device):
+        rc = _lib().xattn_paged_append(
+            K.data_ptr(), V.data_ptr(), ctypes.byref(shape), tokens,
+            XATTN_TOKEN_MAJOR if starts is None else XATTN_HEAD_MAJOR, stride,
+            slots.data_ptr(), None if starts is None else starts.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), _stream(k_pages.device))
+    _raise("xattn_paged_append", rc)
+
+
+def xattn_paged_decode_workspace_bytes(shape: _Paged) -> int:
+    return int(_lib().xattn_paged_decode_workspace_bytes(ctypes.byref(shape)))
+
+
+def xattn_paged_decode(Q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                       table: torch.Tensor, lens: torch.Tensor,
+                       out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] | bool = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Attention of one query token per request over its cached tokens. Q:
+    [nseq, hq, d] (or [nseq, hq, 1, d]); pages [num_pages, hkv, page_size, d];
+    table int32 [nseq, max_pages]; lens int32 [nseq]. Returns O like Q, or (O,
+    lse [nseq, hq]) if lse is True or a tensor."""
+    _check(Q, "Q", k_pages.dtype)
+    _check(table, "table", torch.int32)
+    _check(lens, "lens", torch.int32)
+    if Q.dim() < 3 or Q.numel() != Q.shape[0] * Q.shape[1] * Q.shape[-1]:
+        raise ValueError("Q must be [nseq, hq, d] or [nseq, hq, 1, d]")
+    nseq, hq = Q.shape[0], Q.shape[1]
+    if table.dim() != 2 or table.shape[0] != nseq:
+        raise ValueError("table must be [nseq, max_pages]")
+    _check_shape(lens, (nseq,), "lens")
+    shape = _paged_pair(k_pages, v_pages, hq, nseq, table.shape[1])
+    if Q.shape[-1] != shape.d:
+        raise ValueError("Q and the pages must have the same head size")
+    if out is None:
+        out = torch.empty_like(Q)
+    else:
+        _check(out, "O", Q.dtype)
+        _check_shape(out, Q.shape, "O")
+    want_lse = lse is not None and lse is not False
+    if lse is True:
+        lse = torch.empty(nseq, hq, device=Q.device, dtype=torch.float32)
+    elif want_lse:
+        _check(lse, "lse", torch.float32)
+        _check_shape(lse, (nseq, hq), "lse")
+    if workspace is None:
+        workspace = torch.empty(max(xattn_paged_decode_workspace_bytes(shape), 1),
+                                device=Q.device, dtype=torch.uint8)
+    else:
+        _check(workspace, "workspace")
+    _same_device(Q, k_pages, v_pages, table, lens, out, lse if want_lse else None, workspace)
+    with torch.cuda.device(Q.device):
+        rc = _lib().xattn_paged_decode(
+            Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ctypes.byref(shape),
+            table.data_ptr(), lens.data_ptr(), out.data_ptr(),
+            lse.data_ptr() if want_lse else None, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(Q.device))
+    _raise("xattn_paged_decode", rc)
     return (out, lse) if want_lse else out
 
 

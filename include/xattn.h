@@ -50,6 +50,9 @@
  *   xattn_prefill_host         the whole step on HOST buffers (the one call
  *                              whose tensors may live in host memory)
  *   xattn_prefill_varlen       the whole step on packed variable-length sequences
+ *   xattn_paged_plan           block table and slot map of a paged KV cache
+ *   xattn_paged_append         K and V of new tokens into their cache slots
+ *   xattn_paged_decode         attention of one new token per request over the cache
  *
  * Data types: XATTN_BF16 runs the tensor-core (tcgen05) kernels and needs
  * d = 128 and B = 128. XATTN_F32 runs plain FP32 CUDA-core kernels for small
@@ -71,7 +74,8 @@ typedef enum {
   XATTN_ERR_UNSUPPORTED = -2, /* valid, but outside what the kernels handle */
   XATTN_ERR_CUDA = -3,        /* a CUDA runtime call failed */
   XATTN_ERR_WORKSPACE = -4,   /* workspace pointer NULL or too small */
-  XATTN_ERR_TIMEOUT = -5      /* a kernel's bounded wait ran out (device status) */
+  XATTN_ERR_TIMEOUT = -5,     /* a kernel's bounded wait ran out (device status) */
+  XATTN_ERR_PAGES = -6        /* not enough free pages for a plan (device status) */
 } xattn_status;
 
 typedef enum { XATTN_F32 = 0, XATTN_BF16 = 1 } xattn_dtype;
@@ -399,12 +403,148 @@ int xattn_prefill_varlen(const void* Q, const void* K, const void* V, const xatt
                          int nseq, const int32_t* seqlens, const float* tau, void* O,
                          float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key-value cache: what comes after the prefill.
+ *
+ * The keys and values of nseq requests live in a pool of num_pages pages of
+ * page_size tokens each. Row i of the block table lists the pages of request
+ * i in token order: token t of request i is held by page table[i, t /
+ * page_size], at offset t % page_size. A SLOT is page * page_size + offset.
+ * The free pages sit in a ring of num_pages entries: pool[0] is the position
+ * of the first free page in it, pool[1] how many there are; the j-th free page
+ * is ring[(pool[0] + j) % num_pages].
+ *
+ * One step of a server: xattn_paged_plan (pages and slots for the step's new
+ * tokens), xattn_paged_append (their K and V), xattn_paged_decode (attention
+ * of each request's newest token). None of the three has a counterpart in the
+ * paper. All are capturable in a CUDA graph: every length is read on the
+ * device, so a captured step takes the lengths of the day it is replayed.
+ */
+
+/* Shape of a paged cache. K and V pages have the same shape and strides: the
+ * element (page, KV head, offset, feature) is at page * page_stride + head *
+ * head_stride + offset * token_stride + feature. A contiguous [num_pages, hkv,
+ * page_size, d] array, a [num_pages, page_size, hkv, d] one, or views of one
+ * array that holds K and V are all described by it.
+ * page_size: a power of two from 16 to 256. XATTN_BF16: d 64 or 128;
+ * XATTN_F32: d 32, 64 or 128. hq: a multiple of hkv, at most XATTN_MAX_HEADS.
+ * Strides: in elements, at least d, and multiples of 16 bytes. */
+typedef struct {
+  int nseq;      /* requests (rows of the block table) */
+  int max_pages; /* entries of a block-table row */
+  int num_pages; /* pages of the pool */
+  int page_size, hq, hkv, d, dtype;
+  long long page_stride, head_stride, token_stride;
+} xattn_paged;
+
+/*
+ * Block table and slot map of one step, built on the GPU from the requests'
+ * lengths.
+ *
+ * lens:  int32 [nseq], tokens of each request in the cache.
+ * fresh: int32 [nseq], tokens each request adds in this step; -1 ends it.
+ * pool:  int32 [2], the ring's state before the step.
+ * ring:  in/out, int32 [num_pages]. table: in/out, int32 [nseq, max_pages].
+ * For each request in row order, the pages its new tokens need beyond those
+ * it has are taken from the ring's head and written behind its last page.
+ * A request that ends gives its pages back at the ring's tail (row order,
+ * token order); they can be taken from the next call on. Other entries of
+ * table and ring are left as they were.
+ * lens_out: int32 [nseq], lens + fresh, 0 for a request that ended. May be lens.
+ * pool_out: int32 [2], the ring's state after the step. May be pool.
+ * starts: int32 [nseq + 1], the exclusive prefix sum of max(fresh, 0).
+ * slots:  int32 [max_tokens], the slot of every new token (request i's are
+ *         slots[starts[i] .. starts[i+1]-1], in token order); -1 behind the
+ *         last one. max_tokens >= 0.
+ *
+ * All or nothing: where the step cannot be done the call changes no page and
+ * no length (lens_out = lens, pool_out = pool, table and ring untouched), sets
+ * every slot to -1 and starts to 0, and records the fault, which the next
+ * xattn_get_device_status returns: XATTN_ERR_PAGES when there are not enough
+ * free pages; XATTN_ERR_INVALID_ARG when fresh < -1, lens < 0, a row would
+ * exceed max_pages, the new tokens exceed max_tokens, or pool is not the
+ * state of a ring of num_pages entries. A ring or table entry that is no page
+ * gives its tokens the slot -1 and is reported as XATTN_ERR_INVALID_ARG.
+ * A page belongs to one row: rows that share pages cannot both end.
+ * Errors: INVALID_ARG (NULL pointer, a size below 1, max_tokens < 0),
+ * UNSUPPORTED (page_size, num_pages * page_size or max_pages * page_size above
+ * 2^31 - 1, nseq > 2^20), CUDA.
+ */
+int xattn_paged_plan(int nseq, int page_size, int num_pages, int max_pages, int max_tokens,
+                     const int32_t* lens, const int32_t* fresh, const int32_t* pool,
+                     int32_t* ring, int32_t* table, int32_t* lens_out, int32_t* pool_out,
+                     int32_t* starts, int32_t* slots, void* stream);
+
+/* Layouts of the new tokens' K and V given to xattn_paged_append. */
+typedef enum {
+  XATTN_TOKEN_MAJOR = 0, /* [tokens, hkv, d]; tokens kv_stride elements apart */
+  XATTN_HEAD_MAJOR = 1   /* request i: a [hkv, L_i, d] array starting T_i * hkv * d elements
+                            in, L_i = starts[i+1] - starts[i], T_i = starts[i]: the layout of
+                            xattn_prefill_varlen, and that of a [batch, hkv, L, d] prefill */
+} xattn_kv_layout;
+
+/*
+ * Writes K and V of new tokens to their slots:
+ *   k_pages[slot / page_size, h, slot % page_size, :] = K[token, h, :],
+ * and the same for V. A token whose slot is -1 is left out (rows behind the
+ * last token of a padded batch); a slot outside the pool is left out and
+ * reported by xattn_get_device_status as XATTN_ERR_INVALID_ARG.
+ * cache: shape; hq and max_pages are ignored, nseq only for XATTN_HEAD_MAJOR.
+ * tokens: entries of slots; 0 does nothing.
+ * kv_stride: elements between tokens of K and of V (XATTN_TOKEN_MAJOR only; a
+ *        slice of a fused projection has a stride above hkv * d): at least
+ *        hkv * d and a multiple of 16 bytes. Ignored for XATTN_HEAD_MAJOR.
+ * starts: int32 [nseq + 1] as xattn_paged_plan writes it; only read, and only
+ *        required, for XATTN_HEAD_MAJOR. Tokens at or past starts[nseq] are
+ *        left out.
+ * K, V, k_pages, v_pages: DEVICE, of cache->dtype, 16-byte aligned; k_pages
+ *        and v_pages do not overlap each other or K and V. Slots >= 0 are
+ *        distinct (of two tokens with one slot, either lands, piece by piece).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int xattn_paged_append(const void* K, const void* V, const xattn_paged* cache, int tokens,
+                       int layout, long long kv_stride, const int32_t* slots,
+                       const int32_t* starts, void* k_pages, void* v_pages, void* stream);
+
+/* Bytes of workspace xattn_paged_decode needs. Returns 0 for an invalid shape. */
+size_t xattn_paged_decode_workspace_bytes(const xattn_paged* cache);
+
+/*
+ * Attention of one query token per request over its cached keys and values:
+ *   O[i, h] = sum_t softmax_t(Q[i, h] . K_t / sqrt(d)) V_t,   t < lens[i],
+ * K_t, V_t the rows of token t of request i and KV head h / (hq / hkv). The
+ * newest token's own K and V have to be in the cache (xattn_paged_append
+ * first). A request with lens[i] = 0 gets O = 0 and lse = -inf.
+ *
+ * Q: [nseq, hq, d] contiguous (a [nseq, hq, 1, d] tensor of the other calls);
+ * O: out, like Q. lse: out, optional (may be NULL), fp32 [nseq, hq], the
+ *    natural-log log-sum-exp of the scaled logits. Q, O and both page arrays
+ *    16-byte aligned.
+ * table: int32 [nseq, max_pages]; only the first ceil(lens[i] / page_size)
+ *    entries of row i are read. Rows may share pages. lens: int32 [nseq].
+ *    Both device, read by the kernels. Rows of K and V past lens[i] are not
+ *    read into the result, whatever they hold.
+ * A table entry outside [0, num_pages) leaves its tokens out of the sum; a
+ * length below 0 counts as 0 and one above max_pages * page_size as that; all
+ * are reported by xattn_get_device_status as XATTN_ERR_INVALID_ARG.
+ * ws / ws_bytes: at least xattn_paged_decode_workspace_bytes(cache), 16-byte
+ *    aligned; no contents are expected in it or kept between calls. Calls that
+ *    may overlap on the GPU need a workspace each.
+ * The order of every sum depends on the shape and lengths only: equal inputs
+ * give equal bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+int xattn_paged_decode(const void* Q, const void* k_pages, const void* v_pages,
+                       const xattn_paged* cache, const int32_t* table, const int32_t* lens,
+                       void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's status
  * word. Returns XATTN_OK, XATTN_ERR_TIMEOUT if a kernel gave up a bounded
  * wait since the last call, XATTN_ERR_INVALID_ARG if a selection kernel met a
- * device-resident tau outside (0, 1], or XATTN_ERR_CUDA if the stream reports
- * an error. When several faults happened, the last one recorded is returned.
+ * device-resident tau outside (0, 1] or a paged-cache kernel a length, page or
+ * slot it cannot use, XATTN_ERR_PAGES if a plan ran out of free pages, or
+ * XATTN_ERR_CUDA if the stream reports an error. When several faults happened, the last one recorded is returned.
  */
 int xattn_get_device_status(void* stream);
 
