@@ -40,14 +40,16 @@ constexpr int kMaxCtas = 1024;  // CTAs of the first kernel (bounds the workspac
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A unit's first CTA tells the join who it is and how many CTAs follow it.
+// What the join has to know of a unit: its first CTA and how many CTAs follow
+// it. One entry per unit, or one per first CTA where there are more units.
 struct Split {
-  int request, head, more, pad;
+  int request, head, first, more;
 };
 
 struct DecodeArgs {
   PagedDims D;
   int hc, per;  // chunks the group's heads are cut into, and heads in a chunk
+  bool by_unit; // Split entries are indexed by unit
   const void *Q, *k_pages, *v_pages;
   const int32_t *table, *lens;
   void* O;
@@ -59,8 +61,12 @@ struct DecodeArgs {
   float* part_o;    // [CTA][2][per][d], features in the warps' order
 };
 
-__device__ __forceinline__ int clamped_len(const DecodeArgs& a, int i) {
-  return min(max(a.lens[i], 0), a.D.max_pages << a.D.page_shift);
+__device__ __forceinline__ int clamped(const DecodeArgs& a, int len) {
+  return min(max(len, 0), a.D.max_pages << a.D.page_shift);
+}
+__device__ __forceinline__ Split* split_of(const DecodeArgs& a, int request, int head, int part) {
+  return a.split +
+         (a.by_unit ? (request * a.D.hkv + head) * a.hc + part : static_cast<int>(blockIdx.x));
 }
 
 // ------------------------------------------------------------ loads
@@ -452,6 +458,26 @@ __device__ __forceinline__ unsigned long long range_of(unsigned long long total,
   return total * static_cast<unsigned>(b) / static_cast<unsigned>(groups);
 }
 
+// O = 0 and lse = -inf for the requests that hold nothing.
+template <class Core>
+__device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part, int head0,
+                           int heads) {
+  constexpr int kHalf = Core::kDim / 2;
+  const PagedDims& D = a.D;
+  for (int i = group; i < D.nseq; i += groups) {
+    if (clamped(a, a.lens[i]) != 0) continue;
+    for (int x = threadIdx.x; x < D.hkv * heads * kHalf; x += kWarps * 32) {
+      const int h = x / kHalf, head = h / heads;
+      const long long row =
+          static_cast<long long>(i) * D.hq + head * D.group + head0 + h % heads;
+      store_pair(static_cast<typename Core::T*>(a.O) + row * Core::kDim + x % kHalf * 2, 0.0f,
+                 0.0f);
+      if (x % kHalf == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
+      if (a.by_unit && x % (heads * kHalf) == 0) split_of(a, i, head, part)->more = 0;
+    }
+  }
+}
+
 template <class Core>
 __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const DecodeArgs a) {
   using T = typename Core::T;
@@ -467,7 +493,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
   __shared__ float2 s_ml[kWarps][Core::kHeads];
   __shared__ float s_o[kWarps][Core::kHeads * Core::kRow];
   __shared__ unsigned long long s_sum[kWarps], s_before;
-  __shared__ int s_request;
+  __shared__ int s_request, s_len;
 
   asm volatile("griddepcontrol.launch_dependents;");
 
@@ -476,10 +502,11 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
   const int run = (D.nseq + kThreads - 1) / kThreads;
   const int i0 = min(tid * run, D.nseq), i1 = min(i0 + run, D.nseq);
   unsigned long long mine = 0;
-  bool bad = false;
+  bool bad = false, empty = false;
   for (int i = i0; i < i1; ++i) {
-    const int n = clamped_len(a, i);
-    bad = bad || n != a.lens[i];
+    const int raw = a.lens[i], n = clamped(a, raw);
+    bad = bad || n != raw;
+    empty = empty || n == 0;
     mine += (n + kTile - 1) / kTile;
   }
   if (bad && blockIdx.x == 0) atomicExch(a.status, kStatusBadCache);
@@ -489,60 +516,49 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
     if (lane >= x) upto += y;
   }
   if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
+  empty = __syncthreads_or(empty);
   unsigned long long total = 0;
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) upto += s_sum[w];
     total += s_sum[w];
   }
   total *= D.hkv;
-  // requests that hold nothing
-  for (int i = group; i < D.nseq; i += groups) {
-    if (clamped_len(a, i) != 0) continue;
-    for (int x = tid; x < D.hkv * heads * (kD / 2); x += kThreads) {
-      const int h = x / (kD / 2);
-      const long long row =
-          static_cast<long long>(i) * D.hq + h / heads * D.group + head0 + h % heads;
-      store_pair(static_cast<T*>(a.O) + row * kD + x % (kD / 2) * 2, 0.0f, 0.0f);
-      if (x % (kD / 2) == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
-    }
-  }
-  if (tid == 0) a.split[blockIdx.x].more = 0;
+  if (empty) empty_rows<Core>(a, group, groups, part, head0, heads);
+  if (!a.by_unit && tid == 0) a.split[blockIdx.x].more = 0;
   // as many ranges as there are tiles, at most: none is empty, so a unit's
   // partial results are those of consecutive CTAs
   groups = static_cast<int>(min(static_cast<unsigned long long>(groups), total));
   if (group >= groups) return;
   unsigned long long pos = range_of(total, group, groups);
   const unsigned long long end = range_of(total, group + 1, groups);
-  {
-    unsigned long long before = (upto - mine) * D.hkv;
-    if (pos >= before && pos < upto * D.hkv) {
-      for (int i = i0; i < i1; ++i) {
-        const unsigned long long n =
-            static_cast<unsigned long long>((clamped_len(a, i) + kTile - 1) / kTile) * D.hkv;
-        if (pos < before + n) {
-          s_request = i;
-          s_before = before;
-          break;
-        }
-        before += n;
+  unsigned long long before = (upto - mine) * D.hkv;
+  if (pos >= before && pos < upto * D.hkv) {
+    for (int i = i0; i < i1; ++i) {
+      const int n = clamped(a, a.lens[i]);
+      const unsigned long long next =
+          before + static_cast<unsigned long long>((n + kTile - 1) / kTile) * D.hkv;
+      if (pos < next) {
+        s_request = i;
+        s_len = n;
+        s_before = before;
+        break;
       }
+      before = next;
     }
   }
   __syncthreads();
-  int request = s_request;
-  unsigned long long before = s_before;
+  int request = s_request, len = s_len;
+  before = s_before;
 
   Core core;
   core.init();
   bad = false;
   while (pos < end) {
     // the unit at pos, and this CTA's tiles of it
-    const int len = clamped_len(a, request);
     const int tiles = (len + kTile - 1) / kTile;
     if (pos >= before + static_cast<unsigned long long>(tiles) * D.hkv) {
       before += static_cast<unsigned long long>(tiles) * D.hkv;
-      ++request;
+      len = clamped(a, a.lens[++request]);
       continue;
     }
     const int head = static_cast<int>((pos - before) / tiles);
@@ -638,11 +654,12 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
         if (j == 0) a.part_ml[slot * a.per + h] = make_float2(top, sum);
       }
     }
-    if (tid == 0 && !whole && t0 == 0) {
+    if (tid == 0 && t0 == 0 && (a.by_unit || !whole)) {
       // the group of CTAs whose range holds the unit's last tile
       const unsigned long long last = pos + tiles - 1;
       const int to = static_cast<int>(((last + 1) * groups - 1) / total);
-      a.split[blockIdx.x] = {request, head, to - group, 0};
+      *split_of(a, request, head, part) = {request, head, static_cast<int>(blockIdx.x),
+                                           to - group};
     }
     __syncthreads();
     pos += steps;
@@ -652,58 +669,67 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
 
 constexpr int kJoinWarps = 8;
 
-// Joins the partial results of the unit whose first tiles CTA blockIdx.x had.
-// A warp takes every kJoinWarps-th partial, so their sums have a fixed order.
+// Joins the partial results of a unit for one query head (blockIdx.y). The
+// weights 2^(m - max) are worked out for 32 partials at a time, a lane each;
+// then a warp adds every kJoinWarps-th partial's row, in that order.
 template <typename T, int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a) {
-  constexpr int kPer = kD / 32;
-  __shared__ float s_o[kJoinWarps][kD], s_l[kJoinWarps], s_m[kJoinWarps];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  constexpr int kPer = kD / 32;  // features a lane
+  __shared__ float s_o[kJoinWarps][kD], s_w[kMaxCtas], s_max[kJoinWarps], s_sum[kJoinWarps];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Split s = a.split[blockIdx.x];
   if (s.more == 0) return;
-  const int head0 = static_cast<int>(blockIdx.x % a.hc) * a.per;
-  const int heads = min(a.per, a.D.group - head0);
+  const int head0 = s.first % a.hc * a.per;
+  if (head0 + h >= a.D.group) return;
   auto slot_of = [&](int p) {
-    return (blockIdx.x + static_cast<long long>(p) * a.hc) * 2 + (p == 0 ? 1 : 0);
+    return ((s.first + static_cast<long long>(p) * a.hc) * 2 + (p == 0 ? 1 : 0)) * a.per + h;
   };
-  for (int h = 0; h < heads; ++h) {
-    float m = -INFINITY, l = 0.0f, o[kPer];
-    for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
-    for (int p = warp; p <= s.more; p += kJoinWarps) {
-      const float2 ml = a.part_ml[slot_of(p) * a.per + h];
-      const float* row = a.part_o + (slot_of(p) * a.per + h) * kD + lane * kPer;
-      const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
-      const float f = ex2(m - base), g = ex2(ml.x - base);
-      l = l * f + ml.y * g;
-      for (int j = 0; j < kPer; ++j) o[j] = o[j] * f + row[j] * g;
-      m = top;
-    }
-    if (lane == 0) {
-      s_l[warp] = l;
-      s_m[warp] = m;
-    }
-    for (int j = 0; j < kPer; ++j) s_o[warp][lane * kPer + j] = o[j];
-    __syncthreads();
-    const long long row =
-        static_cast<long long>(s.request) * a.D.hq + s.head * a.D.group + head0 + h;
-    for (int x = threadIdx.x; x < kD / 2; x += kJoinWarps * 32) {
-      float top = -INFINITY, sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
-      for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = ex2(s_m[w] - base);
-        sum += s_l[w] * f;
-        y0 += s_o[w][2 * x] * f;
-        y1 += s_o[w][2 * x + 1] * f;
-      }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      store_pair(static_cast<T*>(a.O) + row * kD + 2 * x, y0 * inv, y1 * inv);
-      if (x == 0 && a.lse != nullptr)
-        a.lse[row] = sum == 0.0f ? -INFINITY : base * kLn2 + logf(sum);
-    }
-    __syncthreads();
+  const int parts = s.more + 1;
+  float m = -INFINITY;
+  for (int p = tid; p < parts; p += kJoinWarps * 32) m = fmaxf(m, a.part_ml[slot_of(p)].x);
+  for (int x = 16; x > 0; x /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  if (lane == 0) s_max[warp] = m;
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_max[w]);
+  const float base = m == -INFINITY ? 0.0f : m;
+  float sum = 0.0f;
+  for (int p = tid; p < parts; p += kJoinWarps * 32) {
+    const float2 ml = a.part_ml[slot_of(p)];
+    const float w = ex2(ml.x - base);
+    s_w[p] = w;
+    sum += ml.y * w;
   }
+  for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  float o[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
+#pragma unroll 4
+  for (int p = warp; p < parts; p += kJoinWarps) {
+    const float* row = a.part_o + slot_of(p) * kD + lane;
+    const float w = s_w[p];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[j] += row[j * 32] * w;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) s_o[warp][j * 32 + lane] = o[j];
+  __syncthreads();
+  const long long row =
+      static_cast<long long>(s.request) * a.D.hq + s.head * a.D.group + head0 + h;
+  if (tid >= kD / 2) return;
+  sum = 0.0f;
+  float2 y = make_float2(0.0f, 0.0f);
+  for (int w = 0; w < kJoinWarps; ++w) {
+    sum += s_sum[w];
+    y.x += s_o[w][2 * tid];
+    y.y += s_o[w][2 * tid + 1];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  store_pair(static_cast<T*>(a.O) + row * kD + 2 * tid, y.x * inv, y.y * inv);
+  if (tid == 0 && a.lse != nullptr)
+    a.lse[row] = sum == 0.0f ? -INFINITY : base * kLn2 + logf(sum);
 }
 
 // ------------------------------------------------------------ host
@@ -730,6 +756,8 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   long long groups = min(static_cast<long long>(num_sms) * Core::kCtas, static_cast<long long>(kMaxCtas)) / a.hc;
   groups = max(1ll, min(groups, tiles));
   const unsigned grid = static_cast<unsigned>(groups * a.hc);
+  const long long units = static_cast<long long>(D.nseq) * D.hkv * a.hc;
+  a.by_unit = units < grid;
   decode_kernel<Core><<<grid, kWarps * 32, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || row_tiles == 1) return e;  // a unit of one tile is never shared
@@ -737,7 +765,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(a.by_unit ? static_cast<unsigned>(units) : grid, a.per);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
@@ -794,7 +822,7 @@ int xattn_paged_decode(const void* Q, const void* k_pages, const void* v_pages,
   const Cut cut = cut_of(D);
   const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * cut.per;
   char* w = static_cast<char*>(ws);
-  DecodeArgs a = {D, cut.hc, cut.per, Q, k_pages, v_pages, table, lens, O, lse, ds->status};
+  DecodeArgs a = {D, cut.hc, cut.per, false, Q, k_pages, v_pages, table, lens, O, lse, ds->status};
   a.split = reinterpret_cast<Split*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + align256(kMaxCtas * sizeof(Split)));
   a.part_o = reinterpret_cast<float*>(w + align256(kMaxCtas * sizeof(Split)) +
