@@ -13,6 +13,10 @@ struct PagedDims {
 
 namespace host {
 
+// 4-D TMA view of a paged cache's K or V (see api.cu).
+int make_pages_map(CUtensorMap* m, const void* ptr, const PagedDims& D, int box_d,
+                   int box_tokens);
+
 // log2 of a page size the kernels take, or -1.
 inline int page_shift_of(int page_size) {
   for (int s = 4; s <= 8; ++s)
@@ -45,7 +49,8 @@ inline int check_paged(const xattn_paged* c, bool with_heads, PagedDims* D) {
   if (!(d == 64 || d == 128 || (d == 32 && c->dtype == XATTN_F32))) return XATTN_ERR_UNSUPPORTED;
   const int esize = c->dtype == XATTN_BF16 ? 2 : 4;
   for (long long s : {c->page_stride, c->head_stride, c->token_stride})
-    if (s < d || s > (1ll << 40) || (s * esize) % 16 != 0) return XATTN_ERR_INVALID_ARG;
+    // (a TMA view's strides are below 2^40 bytes)
+    if (s < d || s >= (1ll << 40) || s * esize >= (1ll << 40) || (s * esize) % 16 != 0) return XATTN_ERR_INVALID_ARG;
   D->nseq = nseq;
   D->max_pages = max_pages;
   D->num_pages = c->num_pages;

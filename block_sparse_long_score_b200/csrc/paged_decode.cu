@@ -19,12 +19,10 @@
 // follows the lengths.
 //
 // Inside a CTA the warps take the tile's chunks, each with its own running
-// maximum, sum and o; they meet once at the end of a unit. K and V go from
-// global memory straight into the registers of the warp that uses them: nothing
-// is shared between warps, so a stage in shared memory would only add a trip.
-// Loads of the next chunk's K are issued when the products with this chunk's
-// are done, V likewise, so a warp has about two chunks' halves in flight and
-// 16 warps an SM cover the memory's latency.
+// maximum, sum and o; they meet once at the end of a unit. A warp's K and V come
+// by TMA through a ring of stages in shared memory of its own, so a stage
+// passes between a warp's lanes only: no CTA-wide barrier in the loop, and the
+// copies run ahead across unit boundaries.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +32,8 @@
 
 namespace xattn {
 namespace {
+
+using host::make_pages_map;
 
 constexpr int kWarps = 4;
 constexpr int kMaxCtas = 1024;  // CTAs of the first kernel (bounds the workspace)
@@ -69,28 +69,11 @@ __device__ __forceinline__ Split* split_of(const DecodeArgs& a, int request, int
          (a.by_unit ? (request * a.D.hkv + head) * a.hc + part : static_cast<int>(blockIdx.x));
 }
 
-// ------------------------------------------------------------ loads
-// 32 bytes a lane. K and V are read once: they are not kept in L1.
-template <bool kWide>
-__device__ __forceinline__ void load32(const char* p, uint32_t* r) {
-  if constexpr (kWide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "l"(p));
-  } else {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p));
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "l"(p + 16));
-  }
-}
-__device__ __forceinline__ void load16(const char* p, uint32_t* r) {
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+__device__ __forceinline__ void read16(uint32_t src, uint32_t* r) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "l"(p));
+               : "r"(src)
+               : "memory");
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -112,25 +95,27 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // products, so that no matrix row is padding when the group is small:
 //   S^T [16 tokens, 8 heads] = K Q^T  and  O^T [d, 8 heads] += V^T P^T
 // with mma.sync m16n8k16 (d / 16 instructions each per 8 heads). tcgen05
-// would want 64 or 128 rows staged in shared memory to feed a product that
-// needs 2 % of its rate; here the operands are in registers already.
+// would want 64 or 128 rows behind descriptors to feed a product that needs
+// 2 % of its rate, and its result back from tensor memory every chunk.
 // The order of the features inside a product is free, as long as both
-// operands agree: lane (r = lane / 4, c = lane % 4) holds the 16 contiguous
-// features 64 j + 16 c .. + 15 of tokens r and r + 8 (K) and of head r (Q),
-// which makes every load 32 contiguous bytes. For V the lane holds features
-// r * d/8 .. of tokens 2c, 2c+1, 2c+8, 2c+9; a byte permutation pairs two
-// tokens' values of a feature. P goes from the accumulator's layout to an
-// operand's with one 8x8 transpose per 8 tokens.
-template <int kD, int NT, bool kWide>
+// operands agree: of each 64 features, lane (r = lane / 4, c = lane % 4) holds
+// 16 c .. + 15 of tokens r and r + 8 (K) and of head r (Q), and 8 r .. + 7 of
+// tokens 2c, 2c+1, 2c+8, 2c+9 (V); a byte permutation pairs two tokens' values
+// of a feature. With TMA's 128-byte swizzle both ways of reading a stage are
+// free of bank conflicts. P goes from the accumulator's layout to an operand's
+// with one 8x8 transpose per 8 tokens.
+template <int kD, int NT>
 struct CoreBf16 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 16;          // tokens of a warp's step
-  static constexpr int kHeads = 8 * NT;      // heads it serves
-  static constexpr int kCtas = (kD == 64 ? 4 : 3) - (NT - 1);  // without spills
+  static constexpr int kBox = 64;            // features of a TMA box: 128 bytes
+  static constexpr int kHalves = kD / 64;
+  static constexpr int kStage = 2 * kChunk * kD * 2;   // K, then V, box after box
+  static constexpr int kParts = NT;                  // a warp's result is joined in parts
+  static constexpr int kBuf = (kD / 16 + 1) * 512;   // of this size
   using T = __nv_bfloat16;
-  static constexpr int kKRegs = kD / 8, kVPer = kD / 16;  // a row's registers a lane: K, V
 
-  uint32_t q[NT][kKRegs], k[2][kKRegs], v[4][kVPer];
+  uint32_t q[NT][8 * kHalves], p[NT][2];
   float o[NT][kD / 16][4], m[NT][2], base[NT][2], l[NT][2];
   int r, c;
 
@@ -143,72 +128,46 @@ struct CoreBf16 {
   __device__ __forceinline__ void start(const DecodeArgs& a, long long q_row, int heads) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const char* p = static_cast<const char*>(a.Q) + (q_row + 8 * t + r) * kD * 2 + c * 32;
+      const uint4* x = static_cast<const uint4*>(a.Q) + (q_row + 8 * t + r) * (kD / 8) + 2 * c;
 #pragma unroll
-      for (int j = 0; j < kD / 64; ++j) {
-        if (8 * t + r < heads) {
-          load16(p + j * 128, &q[t][8 * j]);
-          load16(p + j * 128 + 16, &q[t][8 * j + 4]);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) q[t][8 * j + x] = 0;
-        }
+      for (int j = 0; j < 2 * kHalves; ++j) {
+        const uint4 y =
+            8 * t + r < heads ? x[j / 2 * 8 + j % 2] : make_uint4(0, 0, 0, 0);
+        q[t][4 * j] = y.x, q[t][4 * j + 1] = y.y, q[t][4 * j + 2] = y.z, q[t][4 * j + 3] = y.w;
       }
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[t][i][x] = 0.0f;
+        for (int x4 = 0; x4 < 4; ++x4) o[t][i][x4] = 0.0f;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) m[t][x] = -INFINITY, base[t][x] = 0.0f, l[t][x] = 0.0f;
+      for (int x2 = 0; x2 < 2; ++x2) m[t][x2] = -INFINITY, base[t][x2] = 0.0f, l[t][x2] = 0.0f;
     }
   }
 
-  // Rows past `valid` (< kChunk) take the last valid one's address.
-  __device__ __forceinline__ void load_k(const char* row0, long long stride, int valid) {
-    const int t0 = min(r, valid - 1), t1 = min(r + 8, valid - 1);
-#pragma unroll
-    for (int j = 0; j < kD / 64; ++j) {
-      load32<kWide>(row0 + t0 * stride + j * 128 + c * 32, &k[0][8 * j]);
-      load32<kWide>(row0 + t1 * stride + j * 128 + c * 32, &k[1][8 * j]);
-    }
-  }
-  __device__ __forceinline__ void load_v(const char* row0, long long stride, int valid) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int t = min(2 * c + (x & 1) + (x & 2) * 4, valid - 1);
-      const char* p = row0 + t * stride + r * (kD / 4);
-      if constexpr (kD == 128) load32<kWide>(p, v[x]);
-      else load16(p, v[x]);
-    }
-  }
-  __device__ __forceinline__ void zero_k() {
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int j = 0; j < kKRegs; ++j) k[x][j] = 0;
-  }
-  __device__ __forceinline__ void zero_v() {
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int j = 0; j < kVPer; ++j) v[x][j] = 0;
-  }
-
-  // Weights of the chunk as operands of the second product.
-  uint32_t p[NT][2];
-
-  __device__ __forceinline__ void scores(int valid) {
+  __device__ __forceinline__ void scores(uint32_t stage, int valid) {
     const float scale = kLog2e * (kD == 64 ? 0.125f : 0.08838834764831845f);  // log2(e) / sqrt(d)
     float s[NT][4];
 #pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[t][j] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2 * kHalves; ++j) {
+      uint32_t k0[4], k1[4];
+      const uint32_t at =
+          stage + j / 2 * (kChunk * 128) + r * 128 + (((2 * c + j % 2) ^ r) << 4);
+      read16(at, k0);
+      read16(at + 8 * 128, k1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_bf16(s[t], k0[0], k1[0], k0[1], k1[1], q[t][4 * j], q[t][4 * j + 1]);
+        mma_bf16(s[t], k0[2], k1[2], k0[3], k1[3], q[t][4 * j + 2], q[t][4 * j + 3]);
+      }
+    }
+#pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < kKRegs / 2; ++i)
-        mma_bf16(x, k[0][2 * i], k[1][2 * i], k[0][2 * i + 1], k[1][2 * i + 1], q[t][2 * i],
-                 q[t][2 * i + 1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[t][j] = x[j] * scale;
+      for (int j = 0; j < 4; ++j) s[t][j] *= scale;
       if (valid < kChunk) {
         if (r >= valid) s[t][0] = s[t][1] = -INFINITY;
         if (r + 8 >= valid) s[t][2] = s[t][3] = -INFINITY;
@@ -232,16 +191,7 @@ struct CoreBf16 {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          top = fmaxf(top, m[t][x]);
-          base[t][x] = top == -INFINITY ? 0.0f : top;
-          const float f = ex2(m[t][x] - base[t][x]);
-          m[t][x] = top;
-          l[t][x] *= f;
-#pragma unroll
-          for (int i = 0; i < kD / 16; ++i) {
-            o[t][i][x] *= f;
-            o[t][i][x + 2] *= f;
-          }
+          rescale(t, x, top);
         }
       }
     }
@@ -259,33 +209,76 @@ struct CoreBf16 {
     }
   }
 
-  __device__ __forceinline__ void values(int valid) {
-    if (valid < kChunk) {  // a weight of 0 does not undo a NaN or infinity
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (2 * c + (x & 1) + (x & 2) * 4 >= valid)
-#pragma unroll
-          for (int j = 0; j < kVPer; ++j) v[x][j] = 0;
-    }
+  // Takes the maximum of head (t, x) up to `top`.
+  __device__ __forceinline__ void rescale(int t, int x, float top) {
+    top = fmaxf(top, m[t][x]);
+    base[t][x] = top == -INFINITY ? 0.0f : top;
+    const float f = ex2(m[t][x] - base[t][x]);
+    m[t][x] = top;
+    l[t][x] *= f;
 #pragma unroll
     for (int i = 0; i < kD / 16; ++i) {
-      const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
-      const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
-      const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
-      const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) mma_bf16(o[t][i], a0, a1, a2, a3, p[t][0], p[t][1]);
+      o[t][i][x] *= f;
+      o[t][i][x + 2] *= f;
     }
   }
 
-  // Feature j of a head is at place_of(j) in the joined rows: the lanes' order,
-  // which keeps the stores below free of bank conflicts.
-  __device__ static __forceinline__ int place_of(int j) {
-    return j % (kD / 8) / 2 * 16 + j / (kD / 8) * 2 + j % 2;
+  __device__ __forceinline__ void values(uint32_t stage, int valid) {
+#pragma unroll
+    for (int j = 0; j < kHalves; ++j) {
+      uint32_t v[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = 2 * c + (x & 1);  // and 8 more for x >= 2, the same place modulo 8
+        read16(stage + kStage / 2 + j * (kChunk * 128) + (t + (x & 2) * 4) * 128 + ((r ^ t) << 4),
+               v[x]);
+      }
+      if (valid < kChunk) {  // a weight of 0 does not undo a NaN or infinity
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (2 * c + (x & 1) + (x & 2) * 4 >= valid) v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
+        const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
+        const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
+        const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_bf16(o[t][4 * j + i], a0, a1, a2, a3, p[t][0], p[t][1]);
+      }
+    }
   }
-  static constexpr int kRow = kD + 4;  // a head's row in shared memory, padded likewise
 
-  __device__ __forceinline__ void finish(float2* ml, float* rows) {
+  // Part t of a warp's result to and from a buffer; each lane's share is its own.
+  __device__ __forceinline__ void put(float4* buf, int t) const {
+    buf += threadIdx.x % 32;
+#pragma unroll
+    for (int i = 0; i < kD / 16; ++i)
+      buf[i * 32] = make_float4(o[t][i][0], o[t][i][1], o[t][i][2], o[t][i][3]);
+    buf[kD / 16 * 32] = make_float4(m[t][0], m[t][1], l[t][0], l[t][1]);
+  }
+  __device__ __forceinline__ void merge(const float4* buf, int t) {
+    buf += threadIdx.x % 32;
+    const float4 ml = buf[kD / 16 * 32];
+    rescale(t, 0, ml.x);
+    rescale(t, 1, ml.y);
+    const float f0 = ex2(ml.x - base[t][0]), f1 = ex2(ml.y - base[t][1]);
+    l[t][0] += ml.z * f0;
+    l[t][1] += ml.w * f1;
+#pragma unroll
+    for (int i = 0; i < kD / 16; ++i) {
+      const float4 y = buf[i * 32];
+      o[t][i][0] += y.x * f0;
+      o[t][i][1] += y.y * f1;
+      o[t][i][2] += y.z * f0;
+      o[t][i][3] += y.w * f1;
+    }
+  }
+
+  // The unit's result: to O and lse, or as the partial result at `slot`.
+  __device__ __forceinline__ void emit(const DecodeArgs& a, long long q_row, int heads, bool whole,
+                                       long long slot) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -294,11 +287,32 @@ struct CoreBf16 {
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        if (r == 0) ml[8 * t + 2 * c + x] = make_float2(m[t][x], sum);
+        const int h = 8 * t + 2 * c + x;
+        if (h >= heads) continue;
+        if (whole) {
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          uint4* out = static_cast<uint4*>(a.O) + (q_row + h) * (kD / 8) + r;
 #pragma unroll
-        for (int i = 0; i < kD / 16; ++i)
-          *reinterpret_cast<float2*>(rows + (8 * t + 2 * c + x) * kRow + i * 16 + r * 2) =
-              make_float2(o[t][i][x], o[t][i][x + 2]);
+          for (int j = 0; j < kHalves; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(o[t][4 * j + i][x] * inv, o[t][4 * j + i][x + 2] * inv);
+            out[8 * j] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (r == 0 && a.lse != nullptr)
+            a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base[t][x] * kLn2 + logf(sum);
+        } else {
+          float4* out = reinterpret_cast<float4*>(a.part_o + (slot * a.per + h) * kD) + 2 * r;
+#pragma unroll
+          for (int j = 0; j < kHalves; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              out[16 * j + i] =
+                  make_float4(o[t][4 * j + 2 * i][x], o[t][4 * j + 2 * i][x + 2],
+                              o[t][4 * j + 2 * i + 1][x], o[t][4 * j + 2 * i + 1][x + 2]);
+          if (r == 0) a.part_ml[slot * a.per + h] = make_float2(m[t][x], sum);
+        }
       }
     }
   }
@@ -306,21 +320,23 @@ struct CoreBf16 {
 
 // ------------------------------------------------------------ fp32 core
 // CUDA cores: no tensor-core type keeps fp32's mantissa. A warp's chunk is 8
-// tokens, two to each group of 8 lanes; a lane holds d / 8 features of its two
-// tokens, 16 bytes at a time. The 2 * H dot products of a group are summed
-// over its lanes by halving (one exchange less each step), which leaves one
-// (token, head) logit a lane, so each exponential is taken once.
+// tokens, two (g, g + 4) to each group g of 8 lanes; of every 32 features lane c
+// of a group holds 4 c .. + 3, so a group reads 128 contiguous bytes at a time.
 template <int kD, int H>
 struct CoreF32 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 8;
-  static constexpr int kHeads = H;
-  static constexpr int kCtas = H == 4 ? (kD == 128 ? 2 : 3) : kD == 128 ? 3 : 4;
+  static constexpr int kBox = kD;
+  static constexpr int kPieces = kD / 32;
+  static constexpr int kStage = 2 * kChunk * kD * 4;
+  static constexpr int kPart = H < 2 ? 1 : 2;  // heads joined at a time
+  static constexpr int kParts = H / kPart;
+  static constexpr int kBuf = (kPart * kPieces + 1) * 512;
   using T = float;
   static constexpr int kPer = kD / 8;
 
-  float q[H][kPer], k[2][kPer], v[2][kPer], o[H][kPer], m[H], base[H], l[H], w[2][H];
-  int g, c;  // the lane's group (tokens g and g + 4) and place in it
+  float q[H][kPer], o[H][kPer], m[H], base[H], l[H], w[2][H];
+  int g, c;
 
   __device__ __forceinline__ void init() {
     g = threadIdx.x % 32 / 8;
@@ -341,31 +357,17 @@ struct CoreF32 {
       l[h] = 0.0f;
     }
   }
-  __device__ __forceinline__ void load(const char* row0, long long stride, int valid,
-                                       float (&x)[2][kPer]) {
+  __device__ __forceinline__ void read_rows(uint32_t rows, float (&x)[2][kPer]) const {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int j = 0; j < kPer / 4; ++j)
-        load16(row0 + min(g + 4 * t, valid - 1) * stride + j * 128 + c * 16,
+      for (int j = 0; j < kPieces; ++j)
+        read16(rows + (g + 4 * t) * (kD * 4) + j * 128 + c * 16,
                reinterpret_cast<uint32_t*>(&x[t][4 * j]));
   }
-  __device__ __forceinline__ void load_k(const char* row0, long long stride, int valid) {
-    load(row0, stride, valid, k);
-  }
-  __device__ __forceinline__ void load_v(const char* row0, long long stride, int valid) {
-    load(row0, stride, valid, v);
-  }
-  __device__ __forceinline__ void zero_k() {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) k[0][j] = k[1][j] = 0.0f;
-  }
-  __device__ __forceinline__ void zero_v() {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[0][j] = v[1][j] = 0.0f;
-  }
-  __device__ __forceinline__ void scores(int valid) {
-    float s[2][H];
+  __device__ __forceinline__ void scores(uint32_t stage, int valid) {
+    float k[2][kPer], s[2][H];
+    read_rows(stage, k);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -393,13 +395,7 @@ struct CoreF32 {
         float top = fmaxf(s[0][h], s[1][h]);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        top = fmaxf(top, m[h]);
-        base[h] = top == -INFINITY ? 0.0f : top;
-        const float f = ex2(m[h] - base[h]);
-        m[h] = top;
-        l[h] *= f;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) o[h][j] *= f;
+        rescale(h, top);
       }
     }
 #pragma unroll
@@ -409,7 +405,18 @@ struct CoreF32 {
       l[h] += w[0][h] + w[1][h];
     }
   }
-  __device__ __forceinline__ void values(int valid) {
+  __device__ __forceinline__ void rescale(int h, float top) {
+    top = fmaxf(top, m[h]);
+    base[h] = top == -INFINITY ? 0.0f : top;
+    const float f = ex2(m[h] - base[h]);
+    m[h] = top;
+    l[h] *= f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[h][j] *= f;
+  }
+  __device__ __forceinline__ void values(uint32_t stage, int valid) {
+    float v[2][kPer];
+    read_rows(stage + kStage / 2, v);
     if (valid < kChunk) {  // a weight of 0 does not undo a NaN or infinity
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -423,25 +430,84 @@ struct CoreF32 {
       for (int j = 0; j < kPer; ++j)
         o[h][j] = fmaf(w[1][h], v[1][j], fmaf(w[0][h], v[0][j], o[h][j]));
   }
-  __device__ static __forceinline__ int place_of(int j) { return j; }
-  static constexpr int kRow = kD + 4;
-  __device__ __forceinline__ void finish(float2* ml, float* rows) {
+  __device__ __forceinline__ void put(float4* buf, int part) const {
+    buf += threadIdx.x % 32;
+    float2* ml = reinterpret_cast<float2*>(buf + kPart * kPieces * 32);
+#pragma unroll
+    for (int x = 0; x < kPart; ++x) {
+      const int h = part * kPart + x;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        buf[(x * kPieces + j) * 32] =
+            make_float4(o[h][4 * j], o[h][4 * j + 1], o[h][4 * j + 2], o[h][4 * j + 3]);
+      ml[x] = make_float2(m[h], l[h]);
+    }
+  }
+  __device__ __forceinline__ void merge(const float4* buf, int part) {
+    buf += threadIdx.x % 32;
+    const float2* mls = reinterpret_cast<const float2*>(buf + kPart * kPieces * 32);
+#pragma unroll
+    for (int x = 0; x < kPart; ++x) {
+      const int h = part * kPart + x;
+      const float2 ml = mls[x];
+      rescale(h, ml.x);
+      const float f = ex2(ml.x - base[h]);
+      l[h] += ml.y * f;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const float4 y = buf[(x * kPieces + j) * 32];
+        o[h][4 * j] += y.x * f;
+        o[h][4 * j + 1] += y.y * f;
+        o[h][4 * j + 2] += y.z * f;
+        o[h][4 * j + 3] += y.w * f;
+      }
+    }
+  }
+  __device__ __forceinline__ void emit(const DecodeArgs& a, long long q_row, int heads, bool whole,
+                                       long long slot) {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       float sum = l[h];
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      if (g == 0 && c == 0) ml[h] = make_float2(m[h], sum);
+      if (h >= heads) continue;
+      const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      float* out = whole ? static_cast<float*>(a.O) + (q_row + h) * kD
+                         : a.part_o + (slot * a.per + h) * kD;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        float x = o[h][j];
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (g == 0) rows[h * kRow + j / 4 * 32 + c * 4 + j % 4] = x;
+      for (int j = 0; j < kPieces; ++j) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = o[h][4 * j + i];
+          x[i] += __shfl_xor_sync(0xffffffffu, x[i], 8);
+          x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+        }
+        if (g == j % 4)
+          *reinterpret_cast<float4*>(out + j * 32 + c * 4) =
+              make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      }
+      if (threadIdx.x % 32 == 0) {
+        if (!whole) a.part_ml[slot * a.per + h] = make_float2(m[h], sum);
+        else if (a.lse != nullptr)
+          a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base[h] * kLn2 + logf(sum);
       }
     }
   }
 };
+
+// Stages of a warp's ring: 24 KB a warp where the stages are that large.
+template <class Core>
+constexpr int stages_of() {
+  return 3 * 8192 / Core::kStage < 6 ? 3 * 8192 / Core::kStage : 6;
+}
+// Shared memory of a CTA: the warps' rings (on 1024-byte boundaries, as the
+// swizzle wants them), then two buffers of the join.
+template <class Core>
+constexpr int smem_of() {
+  return 1024 + kWarps * stages_of<Core>() * Core::kStage + 2 * Core::kBuf;
+}
+constexpr int kCtas = 2;  // per SM: two times four rings of 24 KB fill it
 
 // ------------------------------------------------------------ both kernels
 
@@ -479,9 +545,11 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
 }
 
 template <class Core>
-__global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(
+    const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
+    const __grid_constant__ CUtensorMap v_map) {
   using T = typename Core::T;
-  constexpr int kD = Core::kDim, kTile = kWarps * Core::kChunk, kThreads = kWarps * 32;
+  constexpr int kTile = kWarps * Core::kChunk, kThreads = kWarps * 32;
   const PagedDims& D = a.D;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   // CTAs b * hc .. b * hc + hc - 1 take the same tiles for different heads of
@@ -490,12 +558,17 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
   int groups = gridDim.x / a.hc;
   const int head0 = part * a.per, heads = min(a.per, D.group - head0);
 
-  __shared__ float2 s_ml[kWarps][Core::kHeads];
-  __shared__ float s_o[kWarps][Core::kHeads * Core::kRow];
+  constexpr int kStages = stages_of<Core>();
+  extern __shared__ char s_dynamic[];
+  __shared__ uint64_t s_full[kWarps][kStages];
+  __shared__ int s_abort;
   __shared__ unsigned long long s_sum[kWarps], s_before;
   __shared__ int s_request, s_len;
 
   asm volatile("griddepcontrol.launch_dependents;");
+  if (lane < kStages) mbar_init(&s_full[warp][lane], 1);
+  if (tid == 0) s_abort = 0;
+  fence_barrier_init();  // a warp's barriers are used by its own lanes and the TMA unit
 
   // Where this CTA's range begins: a scan of the requests' tile counts, a run
   // of requests to each thread.
@@ -547,124 +620,158 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(const 
     }
   }
   __syncthreads();
-  int request = s_request, len = s_len;
-  before = s_before;
+  // The units of the range in turn. Two of these walk it: one issues copies, the
+  // other, some stages behind, uses them.
+  struct Unit {
+    unsigned long long left;  // tiles of the range from this unit's first on
+    int request, len, head, t0, steps;
+  };
+  auto steps_of = [&](const Unit& u) {
+    const int tiles = (u.len + kTile - 1) / kTile;
+    return static_cast<int>(min(static_cast<unsigned long long>(tiles - u.t0), u.left));
+  };
+  auto next_unit = [&](Unit& u) {  // u.left > u.steps
+    u.left -= u.steps;
+    u.t0 = 0;
+    if (++u.head == D.hkv) {
+      u.head = 0;
+      do u.len = clamped(a, a.lens[++u.request]);
+      while (u.len == 0);
+    }
+    u.steps = steps_of(u);
+  };
+  Unit use;
+  use.left = end - pos;
+  use.request = s_request;
+  use.len = s_len;
+  {
+    const int tiles = (use.len + kTile - 1) / kTile;
+    use.head = static_cast<int>((pos - s_before) / tiles);
+    use.t0 = static_cast<int>((pos - s_before) % tiles);
+  }
+  use.steps = steps_of(use);
+  Unit ahead = use;
 
   Core core;
   core.init();
+  char* rings = s_dynamic + (1024 - smem_u32(s_dynamic) % 1024) % 1024;
+  char* ring = rings + warp * kStages * Core::kStage;
+  float4* bufs = reinterpret_cast<float4*>(rings + kWarps * kStages * Core::kStage);
   bad = false;
-  while (pos < end) {
-    // the unit at pos, and this CTA's tiles of it
-    const int tiles = (len + kTile - 1) / kTile;
-    if (pos >= before + static_cast<unsigned long long>(tiles) * D.hkv) {
-      before += static_cast<unsigned long long>(tiles) * D.hkv;
-      len = clamped(a, a.lens[++request]);
-      continue;
-    }
-    const int head = static_cast<int>((pos - before) / tiles);
-    const int t0 = static_cast<int>((pos - before) % tiles);
-    const int steps = static_cast<int>(min(static_cast<unsigned long long>(tiles - t0), end - pos));
-    const long long q_row = static_cast<long long>(request) * D.hq + head * D.group + head0;
-    const int32_t* pages = a.table + static_cast<long long>(request) * D.max_pages;
-    const long long head_at = head * D.head_stride;
-    const char* k_head = static_cast<const char*>(a.k_pages) + head_at * sizeof(T);
-    const char* v_head = static_cast<const char*>(a.v_pages) + head_at * sizeof(T);
-    const long long stride = D.token_stride * sizeof(T);
 
-    // lane x of a warp holds the page of the warp's step 32 q + x
-    const int first = t0 * kTile + warp * Core::kChunk;  // the warp's first token
-    auto page_batch = [&](int step0) {
-      const int t = first + (step0 + lane) * kTile;
-      if (step0 + lane >= steps || t >= len) return -1;
-      const int page = pages[t >> D.page_shift];
-      if (page >= 0 && page < D.num_pages) return page;
-      bad = true;
-      return -1;
-    };
-    int now = page_batch(0), next = page_batch(32);
-    core.start(a, q_row, heads);
-
-    // a step's tokens: how many are there, and where its rows begin
-    auto rows_of = [&](int step, int* valid) {
-      const int page = __shfl_sync(0xffffffffu, now, step % 32);
-      const int t = first + step * kTile;
-      *valid = page < 0 ? 0 : min(Core::kChunk, len - t);
-      return (page * D.page_stride + (t & (D.page - 1)) * D.token_stride) *
-             static_cast<long long>(sizeof(T));
-    };
-    int valid;
-    long long at = rows_of(0, &valid);
-    if (valid > 0) {
-      core.load_k(k_head + at, stride, valid);
-      core.load_v(v_head + at, stride, valid);
-    } else {
-      core.zero_k();
-      core.zero_v();
-    }
-#pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
-      const int valid_now = valid;
-      core.scores(valid_now);
-      const bool more = step + 1 < steps;
-      if (more) {
-        if ((step + 1) % 32 == 0) {
-          now = next;
-          next = page_batch(step + 33);
+  // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
+  int step = 0, pages = -1, pages_next = -1;
+  auto page_batch = [&](int step0) {
+    const int t = (ahead.t0 + step0 + lane) * kTile + warp * Core::kChunk;
+    if (step0 + lane >= ahead.steps || t >= ahead.len) return -1;
+    const int page = a.table[static_cast<long long>(ahead.request) * D.max_pages +
+                             (t >> D.page_shift)];
+    if (page >= 0 && page < D.num_pages) return page;
+    bad = true;
+    return -1;
+  };
+  pages = page_batch(0);
+  pages_next = page_batch(32);
+  unsigned long long valids = 0;  // rows of the chunks under way, 8 bits each, the newest lowest
+  bool done = false;
+  // Copies the warp's next chunk to a stage.
+  auto issue = [&](int stage) {
+    int valid = 0;
+    if (!done) {
+      const int page = __shfl_sync(0xffffffffu, pages, step % 32);
+      const int t = (ahead.t0 + step) * kTile + warp * Core::kChunk;
+      if (page >= 0) {
+        valid = min(Core::kChunk, ahead.len - t);
+        __syncwarp();  // every lane is done with the stage
+        if (elect_one()) {
+          uint64_t* full = &s_full[warp][stage];
+          char* to = ring + stage * Core::kStage;
+          mbar_arrive_expect_tx(full, Core::kStage);
+#pragma unroll
+          for (int x = 0; x < Core::kDim; x += Core::kBox) {
+            const int at = x * Core::kChunk * static_cast<int>(sizeof(T));
+            tma_load_4d(to + at, &k_map, full, x, t & (D.page - 1), ahead.head, page);
+            tma_load_4d(to + Core::kStage / 2 + at, &v_map, full, x, t & (D.page - 1), ahead.head,
+                        page);
+          }
         }
-        at = rows_of(step + 1, &valid);
-        if (valid > 0) core.load_k(k_head + at, stride, valid);
-        else core.zero_k();
       }
-      core.values(valid_now);
-      if (more) {
-        if (valid > 0) core.load_v(v_head + at, stride, valid);
-        else core.zero_v();
+      if (++step == ahead.steps) {
+        done = ahead.left == static_cast<unsigned long long>(ahead.steps);
+        if (!done) {
+          next_unit(ahead);
+          step = 0;
+          pages = page_batch(0);
+          pages_next = page_batch(32);
+        }
+      } else if (step % 32 == 0) {
+        pages = pages_next;
+        pages_next = page_batch(step + 32);
       }
+    }
+    valids = valids << 8 | static_cast<unsigned>(valid);
+  };
+  for (int x = 0; x < kStages; ++x) issue(x);
+
+  int stage = 0;
+  uint32_t phases = 0;  // parity of each stage's next wait
+  bool lost = false;    // a wait ran out
+  while (true) {
+    const int tiles = (use.len + kTile - 1) / kTile;
+    const long long q_row =
+        static_cast<long long>(use.request) * D.hq + use.head * D.group + head0;
+    core.start(a, q_row, heads);
+#pragma unroll 1
+    for (int x = 0; x < use.steps; ++x) {
+      const int valid = static_cast<int>(valids >> (8 * (kStages - 1))) & 255;
+      if (valid > 0) {
+        uint64_t* full = &s_full[warp][stage];
+        const uint32_t phase = phases >> stage & 1;
+        if (!warp_wait(full, phase, &s_abort)) {
+          // this or another warp's wait ran out: issue no more, and wait once
+          // more, bounded again, for what is in flight; the status tells
+          lost = done = true;
+          volatile int own = 0;
+          warp_wait(full, phase, &own);
+        }
+        phases ^= 1u << stage;
+        const uint32_t at = smem_u32(ring + stage * Core::kStage);
+        core.scores(at, valid);
+        core.values(at, valid);
+      }
+      issue(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
-    // the warps' results of this unit, joined
-    core.finish(s_ml[warp], s_o[warp]);
-    __syncthreads();
-    const bool whole = t0 == 0 && steps == tiles;
-    const long long slot = blockIdx.x * 2ll + (t0 == 0 ? 1 : 0);
-    for (int x = tid; x < heads * (kD / 2); x += kThreads) {
-      const int h = x / (kD / 2), j = x % (kD / 2) * 2;
-      float top = s_ml[0][h].x;
+    // the warps' results of this unit, joined in a fixed order: 0 + 2, 1 + 3, then both
+    float4* mine_buf = bufs + warp % 2 * (Core::kBuf / 16);
+    float4* other_buf = bufs + Core::kBuf / 16;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][h].x);
-      const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f;
-      float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_ml[w][h].x - base);
-        const float2 y =
-            *reinterpret_cast<const float2*>(&s_o[w][h * Core::kRow + Core::place_of(j)]);
-        sum += s_ml[w][h].y * f;
-        o.x += y.x * f;
-        o.y += y.y * f;
-      }
-      if (whole) {
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        store_pair(static_cast<T*>(a.O) + (q_row + h) * kD + j, o.x * inv, o.y * inv);
-        if (j == 0 && a.lse != nullptr)
-          a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base * kLn2 + logf(sum);
-      } else {
-        *reinterpret_cast<float2*>(&a.part_o[(slot * a.per + h) * kD + j]) = o;
-        if (j == 0) a.part_ml[slot * a.per + h] = make_float2(top, sum);
+    for (int x = 0; x < Core::kParts; ++x) {
+      __syncthreads();
+      if (warp >= 2) core.put(mine_buf, x);
+      __syncthreads();
+      if (warp < 2) core.merge(mine_buf, x);
+      if (warp == 1) core.put(mine_buf, x);
+      __syncthreads();
+      if (warp == 0) core.merge(other_buf, x);
+    }
+    if (warp == 0) {
+      core.emit(a, q_row, heads, use.t0 == 0 && use.steps == tiles,
+                blockIdx.x * 2ll + (use.t0 == 0 ? 1 : 0));
+      if (lane == 0 && use.t0 == 0 && (a.by_unit || use.steps < tiles)) {
+        // the group of CTAs whose range holds the unit's last tile
+        const unsigned long long last = end - use.left + tiles - 1;
+        const int to = static_cast<int>(((last + 1) * groups - 1) / total);
+        *split_of(a, use.request, use.head, part) = {use.request, use.head,
+                                                     static_cast<int>(blockIdx.x), to - group};
       }
     }
-    if (tid == 0 && t0 == 0 && (a.by_unit || !whole)) {
-      // the group of CTAs whose range holds the unit's last tile
-      const unsigned long long last = pos + tiles - 1;
-      const int to = static_cast<int>(((last + 1) * groups - 1) / total);
-      *split_of(a, request, head, part) = {request, head, static_cast<int>(blockIdx.x),
-                                           to - group};
-    }
-    __syncthreads();
-    pos += steps;
+    if (use.left == static_cast<unsigned long long>(use.steps)) break;
+    next_unit(use);
   }
   if (bad) atomicExch(a.status, kStatusBadCache);
+  if (lost && lane == 0) atomicExch(a.status, kStatusTimeout);
 }
 
 constexpr int kJoinWarps = 8;
@@ -753,13 +860,21 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   // no more groups than tiles there can be
   const long long row_tiles = ((static_cast<long long>(D.max_pages) << D.page_shift) + kTile - 1) / kTile;
   const long long tiles = row_tiles * D.nseq * D.hkv;
-  long long groups = min(static_cast<long long>(num_sms) * Core::kCtas, static_cast<long long>(kMaxCtas)) / a.hc;
+  long long groups = min(static_cast<long long>(num_sms) * kCtas, static_cast<long long>(kMaxCtas)) / a.hc;
   groups = max(1ll, min(groups, tiles));
   const unsigned grid = static_cast<unsigned>(groups * a.hc);
   const long long units = static_cast<long long>(D.nseq) * D.hkv * a.hc;
   a.by_unit = units < grid;
-  decode_kernel<Core><<<grid, kWarps * 32, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_of<Core>());
+  if (e != cudaSuccess) return e;
+  CUtensorMap k_map, v_map;
+  if (make_pages_map(&k_map, a.k_pages, D, Core::kBox, Core::kChunk) != XATTN_OK ||
+      make_pages_map(&v_map, a.v_pages, D, Core::kBox, Core::kChunk) != XATTN_OK)
+    return cudaErrorInvalidValue;
+  decode_kernel<Core><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
+  e = cudaGetLastError();
   if (e != cudaSuccess || row_tiles == 1) return e;  // a unit of one tile is never shared
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -774,12 +889,9 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
 }
 
 template <int kD>
-cudaError_t launch_bf16(const DecodeArgs& a, bool wide, int num_sms, cudaStream_t st) {
-  if (a.per <= 8)
-    return wide ? launch_decode<CoreBf16<kD, 1, true>>(a, num_sms, st)
-                : launch_decode<CoreBf16<kD, 1, false>>(a, num_sms, st);
-  return wide ? launch_decode<CoreBf16<kD, 2, true>>(a, num_sms, st)
-              : launch_decode<CoreBf16<kD, 2, false>>(a, num_sms, st);
+cudaError_t launch_bf16(const DecodeArgs& a, int num_sms, cudaStream_t st) {
+  return a.per <= 8 ? launch_decode<CoreBf16<kD, 1>>(a, num_sms, st)
+                    : launch_decode<CoreBf16<kD, 2>>(a, num_sms, st);
 }
 
 template <int kD>
@@ -829,14 +941,8 @@ int xattn_paged_decode(const void* Q, const void* k_pages, const void* v_pages,
                                       align256(rows * sizeof(float2)));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (D.dtype == XATTN_BF16) {
-    // 32-byte loads need every row on a 32-byte boundary
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(k_pages) |
-                           reinterpret_cast<uintptr_t>(v_pages) |
-                           static_cast<uintptr_t>(
-                               (D.page_stride | D.head_stride | D.token_stride) * D.esize);
-    const bool wide = (bits & 31u) == 0;
-    return cuda_status(D.d == 64 ? launch_bf16<64>(a, wide, ds->num_sms, st)
-                                 : launch_bf16<128>(a, wide, ds->num_sms, st));
+    return cuda_status(D.d == 64 ? launch_bf16<64>(a, ds->num_sms, st)
+                                 : launch_bf16<128>(a, ds->num_sms, st));
   }
   return cuda_status(D.d == 32   ? launch_f32<32>(a, ds->num_sms, st)
                      : D.d == 64 ? launch_f32<64>(a, ds->num_sms, st)
