@@ -76,6 +76,19 @@ __device__ __forceinline__ void read16(uint32_t src, uint32_t* r) {
                : "memory");
 }
 
+__device__ __forceinline__ void ldmatrix(uint32_t src, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t src, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(src)
+               : "memory");
+}
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -97,44 +110,46 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // with mma.sync m16n8k16 (d / 16 instructions each per 8 heads). tcgen05
 // would want 64 or 128 rows behind descriptors to feed a product that needs
 // 2 % of its rate, and its result back from tensor memory every chunk.
-// The order of the features inside a product is free, as long as both
-// operands agree: of each 64 features, lane (r = lane / 4, c = lane % 4) holds
-// 16 c .. + 15 of tokens r and r + 8 (K) and of head r (Q), and 8 r .. + 7 of
-// tokens 2c, 2c+1, 2c+8, 2c+9 (V); a byte permutation pairs two tokens' values
-// of a feature. With TMA's 128-byte swizzle both ways of reading a stage are
-// free of bank conflicts. P goes from the accumulator's layout to an operand's
-// with one 8x8 transpose per 8 tokens.
+// ldmatrix brings both operands from TMA's 128-byte swizzle without bank
+// conflicts, V transposed on the way; P goes from the accumulator's layout to an
+// operand's with one 8x8 transpose per 8 tokens. A lane is (r, c) = (lane / 4,
+// lane % 4): tokens r and r + 8 and heads 2c, 2c + 1 of S^T, features r and
+// r + 8 of every 16 of O^T.
 template <int kD, int NT>
 struct CoreBf16 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 16;          // tokens of a warp's step
   static constexpr int kBox = 64;            // features of a TMA box: 128 bytes
-  static constexpr int kHalves = kD / 64;
+  // three CTAs an SM with two 8 KB stages a warp, or two with three
+  static constexpr int kCtas = NT == 1 ? 3 : 2, kRing = NT == 1 ? 16384 : 24576;
   static constexpr int kStage = 2 * kChunk * kD * 2;   // K, then V, box after box
   static constexpr int kParts = NT;                  // a warp's result is joined in parts
   static constexpr int kBuf = (kD / 16 + 1) * 512;   // of this size
   using T = __nv_bfloat16;
 
-  uint32_t q[NT][8 * kHalves], p[NT][2];
+  uint32_t q[NT][kD / 8], p[NT][2];
   float o[NT][kD / 16][4], m[NT][2], base[NT][2], l[NT][2];
   int r, c;
+  // This lane's row of the four 8x8 matrices of an ldmatrix, at the first 16
+  // features; the next 16 are a xor with 32 further.
+  uint32_t k_at, v_at;
 
   __device__ __forceinline__ void init() {
-    r = threadIdx.x % 32 / 4;
-    c = threadIdx.x % 4;
+    const uint32_t lane = threadIdx.x % 32;
+    r = lane / 4;
+    c = lane % 4;
+    // K: (tokens 0-7, 8-15) x (features 0-7, 8-15); V: features vary first
+    k_at = lane % 16 * 128 + ((lane / 16 ^ lane % 8) << 4);
+    v_at = (lane % 8 + lane / 16 * 8) * 128 + ((lane / 8 % 2 ^ lane % 8) << 4);
   }
 
   // Heads of the unit; rows past the chunk's heads are zero.
   __device__ __forceinline__ void start(const DecodeArgs& a, long long q_row, int heads) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const uint4* x = static_cast<const uint4*>(a.Q) + (q_row + 8 * t + r) * (kD / 8) + 2 * c;
+      const uint32_t* x = static_cast<const uint32_t*>(a.Q) + (q_row + 8 * t + r) * (kD / 2) + c;
 #pragma unroll
-      for (int j = 0; j < 2 * kHalves; ++j) {
-        const uint4 y =
-            8 * t + r < heads ? x[j / 2 * 8 + j % 2] : make_uint4(0, 0, 0, 0);
-        q[t][4 * j] = y.x, q[t][4 * j + 1] = y.y, q[t][4 * j + 2] = y.z, q[t][4 * j + 3] = y.w;
-      }
+      for (int j = 0; j < kD / 8; ++j) q[t][j] = 8 * t + r < heads ? x[4 * j] : 0;
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i)
 #pragma unroll
@@ -146,28 +161,24 @@ struct CoreBf16 {
 
   __device__ __forceinline__ void scores(uint32_t stage, int valid) {
     const float scale = kLog2e * (kD == 64 ? 0.125f : 0.08838834764831845f);  // log2(e) / sqrt(d)
-    float s[NT][4];
+    // even and odd steps of 16 features sum apart: two chains half as long
+    float s[NT][4], s1[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[t][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) s[t][j] = s1[t][j] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 2 * kHalves; ++j) {
-      uint32_t k0[4], k1[4];
-      const uint32_t at =
-          stage + j / 2 * (kChunk * 128) + r * 128 + (((2 * c + j % 2) ^ r) << 4);
-      read16(at, k0);
-      read16(at + 8 * 128, k1);
+    for (int i = 0; i < kD / 16; ++i) {
+      uint32_t k[4];
+      ldmatrix(stage + i / 4 * (kChunk * 128) + (k_at ^ i % 4 * 32), k);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        mma_bf16(s[t], k0[0], k1[0], k0[1], k1[1], q[t][4 * j], q[t][4 * j + 1]);
-        mma_bf16(s[t], k0[2], k1[2], k0[3], k1[3], q[t][4 * j + 2], q[t][4 * j + 3]);
-      }
+      for (int t = 0; t < NT; ++t)
+        mma_bf16(i % 2 ? s1[t] : s[t], k[0], k[1], k[2], k[3], q[t][2 * i], q[t][2 * i + 1]);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[t][j] *= scale;
+      for (int j = 0; j < 4; ++j) s[t][j] = (s[t][j] + s1[t][j]) * scale;
       if (valid < kChunk) {
         if (r >= valid) s[t][0] = s[t][1] = -INFINITY;
         if (r + 8 >= valid) s[t][2] = s[t][3] = -INFINITY;
@@ -225,28 +236,17 @@ struct CoreBf16 {
 
   __device__ __forceinline__ void values(uint32_t stage, int valid) {
 #pragma unroll
-    for (int j = 0; j < kHalves; ++j) {
-      uint32_t v[4][4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int t = 2 * c + (x & 1);  // and 8 more for x >= 2, the same place modulo 8
-        read16(stage + kStage / 2 + j * (kChunk * 128) + (t + (x & 2) * 4) * 128 + ((r ^ t) << 4),
-               v[x]);
-      }
+    for (int i = 0; i < kD / 16; ++i) {
+      uint32_t v[4];
+      ldmatrix_trans(stage + kStage / 2 + i / 4 * (kChunk * 128) + (v_at ^ i % 4 * 32), v);
       if (valid < kChunk) {  // a weight of 0 does not undo a NaN or infinity
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (2 * c + (x & 1) + (x & 2) * 4 >= valid) v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0;
+        const uint32_t low = 2 * c < valid ? (2 * c + 1 < valid ? ~0u : 0xffffu) : 0;
+        const uint32_t high = 2 * c + 8 < valid ? (2 * c + 9 < valid ? ~0u : 0xffffu) : 0;
+        v[0] &= low, v[1] &= low, v[2] &= high, v[3] &= high;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
-        const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
-        const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
-        const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma_bf16(o[t][4 * j + i], a0, a1, a2, a3, p[t][0], p[t][1]);
-      }
+      for (int t = 0; t < NT; ++t)
+        mma_bf16(o[t][i], v[0], v[1], v[2], v[3], p[t][0], p[t][1]);
     }
   }
 
@@ -291,26 +291,21 @@ struct CoreBf16 {
         if (h >= heads) continue;
         if (whole) {
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          uint4* out = static_cast<uint4*>(a.O) + (q_row + h) * (kD / 8) + r;
+          T* out = static_cast<T*>(a.O) + (q_row + h) * kD + r;
 #pragma unroll
-          for (int j = 0; j < kHalves; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(o[t][4 * j + i][x] * inv, o[t][4 * j + i][x + 2] * inv);
-            out[8 * j] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < kD / 16; ++i) {
+            out[16 * i] = __float2bfloat16_rn(o[t][i][x] * inv);
+            out[16 * i + 8] = __float2bfloat16_rn(o[t][i][x + 2] * inv);
           }
           if (r == 0 && a.lse != nullptr)
             a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base[t][x] * kLn2 + logf(sum);
         } else {
-          float4* out = reinterpret_cast<float4*>(a.part_o + (slot * a.per + h) * kD) + 2 * r;
+          float* out = a.part_o + (slot * a.per + h) * kD + r;
 #pragma unroll
-          for (int j = 0; j < kHalves; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              out[16 * j + i] =
-                  make_float4(o[t][4 * j + 2 * i][x], o[t][4 * j + 2 * i][x + 2],
-                              o[t][4 * j + 2 * i + 1][x], o[t][4 * j + 2 * i + 1][x + 2]);
+          for (int i = 0; i < kD / 16; ++i) {
+            out[16 * i] = o[t][i][x];
+            out[16 * i + 8] = o[t][i][x + 2];
+          }
           if (r == 0) a.part_ml[slot * a.per + h] = make_float2(m[t][x], sum);
         }
       }
@@ -327,6 +322,7 @@ struct CoreF32 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 8;
   static constexpr int kBox = kD;
+  static constexpr int kCtas = H == 4 ? 2 : 3, kRing = H == 4 ? 24576 : 16384;
   static constexpr int kPieces = kD / 32;
   static constexpr int kStage = 2 * kChunk * kD * 4;
   static constexpr int kPart = H < 2 ? 1 : 2;  // heads joined at a time
@@ -496,10 +492,10 @@ struct CoreF32 {
   }
 };
 
-// Stages of a warp's ring: 24 KB a warp where the stages are that large.
+// Stages of a warp's ring: kRing bytes a warp where the stages are that large.
 template <class Core>
 constexpr int stages_of() {
-  return 3 * 8192 / Core::kStage < 6 ? 3 * 8192 / Core::kStage : 6;
+  return Core::kRing / Core::kStage < 6 ? Core::kRing / Core::kStage : 6;
 }
 // Shared memory of a CTA: the warps' rings (on 1024-byte boundaries, as the
 // swizzle wants them), then two buffers of the join.
@@ -507,8 +503,6 @@ template <class Core>
 constexpr int smem_of() {
   return 1024 + kWarps * stages_of<Core>() * Core::kStage + 2 * Core::kBuf;
 }
-constexpr int kCtas = 2;  // per SM: two times four rings of 24 KB fill it
-
 // ------------------------------------------------------------ both kernels
 
 __device__ __forceinline__ void store_pair(float* p, float x, float y) {
@@ -545,7 +539,7 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
 }
 
 template <class Core>
-__global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(
+__global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using T = typename Core::T;
@@ -672,7 +666,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(
   };
   pages = page_batch(0);
   pages_next = page_batch(32);
-  unsigned long long valids = 0;  // rows of the chunks under way, 8 bits each, the newest lowest
+  uint32_t valids = 0;  // rows of the chunks under way, 5 bits each, the newest lowest
   bool done = false;
   // Copies the warp's next chunk to a stage.
   auto issue = [&](int stage) {
@@ -709,7 +703,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(
         pages_next = page_batch(step + 32);
       }
     }
-    valids = valids << 8 | static_cast<unsigned>(valid);
+    valids = valids << 5 | static_cast<unsigned>(valid);
   };
   for (int x = 0; x < kStages; ++x) issue(x);
 
@@ -723,7 +717,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(
     core.start(a, q_row, heads);
 #pragma unroll 1
     for (int x = 0; x < use.steps; ++x) {
-      const int valid = static_cast<int>(valids >> (8 * (kStages - 1))) & 255;
+      const int valid = static_cast<int>(valids >> (5 * (kStages - 1)) & 31);
       if (valid > 0) {
         uint64_t* full = &s_full[warp][stage];
         const uint32_t phase = phases >> stage & 1;
@@ -860,7 +854,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   // no more groups than tiles there can be
   const long long row_tiles = ((static_cast<long long>(D.max_pages) << D.page_shift) + kTile - 1) / kTile;
   const long long tiles = row_tiles * D.nseq * D.hkv;
-  long long groups = min(static_cast<long long>(num_sms) * kCtas, static_cast<long long>(kMaxCtas)) / a.hc;
+  long long groups = min(static_cast<long long>(num_sms) * Core::kCtas, static_cast<long long>(kMaxCtas)) / a.hc;
   groups = max(1ll, min(groups, tiles));
   const unsigned grid = static_cast<unsigned>(groups * a.hc);
   const long long units = static_cast<long long>(D.nseq) * D.hkv * a.hc;
