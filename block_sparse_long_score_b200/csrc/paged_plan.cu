@@ -1,14 +1,34 @@
 // paged_plan.cu -- xattn_paged_plan: block table and slot map of a paged cache,
 // built on the GPU from the requests' lengths.
+//
+// With have = ceil(len / P), need = ceil((len + grow) / P) - have and the exclusive
+// prefix sums tok, off, rel of grow, need and the pages given back, over the
+// requests in row order:
+//   table[i, have + j]               = ring[head + off_i + j],  j < need_i
+//   ring[head + free + rel_i + j]    = table[i, j],             j < have_i, if i ends
+//   slots[tok_i + t]                 = page * P + (len_i + t) % P,
+// the page of a token being table's where the request had it and the ring's where it
+// is new, so no output waits for another. The call moves a few bytes a
+// request, page and token and is bound by latency: the launch, the read of the
+// lengths, two barriers a scan and one read of a page id.
+//
+// One launch of one cluster. Every CTA reads all lengths and does the scans for
+// itself (a few us less than passing them on), then the cluster's threads share
+// the pages and tokens out by their number in the sums, whoever the request: each
+// finds its request by bisection of the sums in shared memory. Lengths and the
+// ring's state may be updated in place, so they are written last, behind a
+// cluster barrier that tells that every CTA has read them.
 #include <cuda_runtime.h>
 
 #include "host.cuh"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace xattn {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024;  // also the requests of a scan
+constexpr int kMostCtas = 16;   // of the cluster
 
 struct PlanArgs {
   int nseq, shift, num_pages, max_pages, max_tokens;
@@ -43,108 +63,175 @@ __device__ __forceinline__ Change change_of(const PlanArgs& a, int i) {
   return c;
 }
 
-// Inclusive scan of a 64-bit value over the block; *total gets the block's sum.
-__device__ long long block_scan(long long v, long long* total) {
-  __shared__ long long part[33];
+struct Sums {
+  long long tok, need, back;
+};
+__device__ __forceinline__ Sums operator+(const Sums& x, const Sums& y) {
+  return {x.tok + y.tok, x.need + y.need, x.back + y.back};
+}
+
+// Inclusive sums over the block's threads; *total gets the block's.
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* total) {
+  __shared__ Sums part[32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int o = 1; o < 32; o *= 2) {
-    const long long w = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += w;
-  }
-  __syncthreads();
+  auto warp_scan = [&](Sums x) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const Sums y = {__shfl_up_sync(0xffffffffu, x.tok, o),
+                      __shfl_up_sync(0xffffffffu, x.need, o),
+                      __shfl_up_sync(0xffffffffu, x.back, o)};
+      if (lane >= o) x = x + y;
+    }
+    return x;
+  };
+  v = warp_scan(v);
+  __syncthreads();  // the last call's readers are done
   if (lane == 31) part[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    long long p = part[lane];
-    for (int o = 1; o < 32; o *= 2) {
-      const long long w = __shfl_up_sync(0xffffffffu, p, o);
-      if (lane >= o) p += w;
-    }
-    part[lane] = p;
+  const Sums p = warp_scan(part[lane]);  // every warp for itself: one barrier less
+  *total = {__shfl_sync(0xffffffffu, p.tok, 31), __shfl_sync(0xffffffffu, p.need, 31),
+            __shfl_sync(0xffffffffu, p.back, 31)};
+  const int before = max(warp - 1, 0);
+  const Sums q = {__shfl_sync(0xffffffffu, p.tok, before),
+                  __shfl_sync(0xffffffffu, p.need, before),
+                  __shfl_sync(0xffffffffu, p.back, before)};
+  return warp > 0 ? v + q : v;
+}
+
+// The last of n sums that is at or below x, of those with sums[0] <= x < sums[n].
+__device__ __forceinline__ int find(const int* sums, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (sums[mid] <= x) lo = mid;
+    else hi = mid - 1;
   }
-  __syncthreads();
-  *total = part[31];
-  return v + (warp > 0 ? part[warp - 1] : 0);
+  return lo;
 }
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
+  __shared__ int s_tok[kThreads + 1], s_need[kThreads + 1], s_back[kThreads + 1];
+  __shared__ int s_len[kThreads];
   const int tid = threadIdx.x;
+  const int all = gridDim.x * kThreads, me = blockIdx.x * kThreads + tid;  // of the cluster
   const int head = a.pool[0], free_pages = a.pool[1];
-  // whether the step can be done, from the totals
-  long long tokens = 0, need = 0, back = 0, bad = 0;
-  for (int i0 = 0; i0 < a.nseq; i0 += kThreads) {
-    const Change c = change_of(a, i0 + tid);
-    tokens += c.grow;
-    need += c.need;
-    back += c.back;
-    bad += c.bad;
+  const bool one_scan = a.nseq <= kThreads;
+
+  // the step's totals, and whether it can be done
+  Change c = change_of(a, tid);
+  Sums sum = {c.grow, c.need, c.back}, total;
+  bool bad = c.bad;
+  for (int i = tid + kThreads; i < a.nseq; i += kThreads) {
+    const Change d = change_of(a, i);
+    sum = sum + Sums{d.grow, d.need, d.back};
+    bad = bad || d.bad;
   }
-  long long all_tokens, all_need, all_back, all_bad;
-  block_scan(tokens, &all_tokens);
-  block_scan(need, &all_need);
-  block_scan(back, &all_back);
-  block_scan(bad, &all_bad);
-  const bool wrong = all_bad != 0 || all_tokens > a.max_tokens || head < 0 ||
+  sum = block_scan(sum, &total);
+  const bool wrong = __syncthreads_or(bad) || total.tok > a.max_tokens || head < 0 ||
                      head >= a.num_pages || free_pages < 0 ||
-                     free_pages + all_back > a.num_pages;
-  const bool lacking = !wrong && all_need > free_pages;
+                     free_pages + total.back > a.num_pages;
+  const bool lacking = !wrong && total.need > free_pages;
   if (wrong || lacking) {
-    for (int i = tid; i < a.nseq; i += kThreads) a.lens_out[i] = a.lens[i];
-    for (int i = tid; i <= a.nseq; i += kThreads) a.starts[i] = 0;
-    for (int t = tid; t < a.max_tokens; t += kThreads) a.slots[t] = -1;
-    if (tid == 0) {
+    for (unsigned t = me; t < static_cast<unsigned>(a.max_tokens); t += all) a.slots[t] = -1;
+    for (int i = me; i <= a.nseq; i += all) a.starts[i] = 0;
+    for (int i = me; i < a.nseq; i += all) a.lens_out[i] = a.lens[i];
+    if (me == 0) {
       a.pool_out[0] = head;
       a.pool_out[1] = free_pages;
       atomicExch(a.status, wrong ? kStatusBadCache : kStatusNoPages);
     }
     return;
   }
-  long long token0 = 0, need0 = 0, back0 = 0;
+
+  // position x of the ring, counted from its head (x <= num_pages)
+  auto ring_at = [&](int x) -> int32_t& {
+    x += head;
+    return a.ring[x >= a.num_pages ? x - a.num_pages : x];
+  };
   bool bad_page = false;
+  Sums before = {0, 0, 0};
   for (int i0 = 0; i0 < a.nseq; i0 += kThreads) {
-    const int i = i0 + tid;
-    const Change c = change_of(a, i);
-    long long sum;
-    const long long t_at = token0 + block_scan(c.grow, &sum) - c.grow;
-    token0 += sum;
-    const long long n_at = need0 + block_scan(c.need, &sum) - c.need;
-    need0 += sum;
-    const long long b_at = back0 + block_scan(c.back, &sum) - c.back;
-    back0 += sum;
-    if (i >= a.nseq) continue;
-    int32_t* row = a.table + static_cast<long long>(i) * a.max_pages;
-    for (int j = 0; j < c.need; ++j)
-      row[c.have + j] = a.ring[(head + n_at + j) % a.num_pages];
-    for (int j = 0; j < c.back; ++j)
-      a.ring[(head + free_pages + b_at + j) % a.num_pages] = row[j];
-    a.starts[i] = static_cast<int32_t>(t_at);
-    a.lens_out[i] = c.back > 0 ? 0 : c.len + c.grow;
-  }
-  if (tid == 0) {
-    a.starts[a.nseq] = static_cast<int32_t>(all_tokens);
-    a.pool_out[0] = static_cast<int32_t>((head + all_need) % a.num_pages);
-    a.pool_out[1] = static_cast<int32_t>(free_pages - all_need + all_back);
-  }
-  __syncthreads();
-  for (int t = tid; t < a.max_tokens; t += kThreads) {
-    int slot = -1;
-    if (t < all_tokens) {
-      int lo = 0, hi = a.nseq - 1;  // the last request whose start is at or before t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.starts[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      const int at = a.starts[lo];
-      const int pos = a.lens_out[lo] - (a.starts[lo + 1] - at) + (t - at);
-      const int page = a.table[static_cast<long long>(lo) * a.max_pages + (pos >> a.shift)];
-      if (page >= 0 && page < a.num_pages)
-        slot = (page << a.shift) + (pos & ((1 << a.shift) - 1));
-      else
-        bad_page = true;
+    const int n = min(kThreads, a.nseq - i0);
+    if (!one_scan) {
+      c = change_of(a, i0 + tid);
+      sum = before + block_scan({c.grow, c.need, c.back}, &total);
+      before = before + total;
     }
-    a.slots[t] = slot;
+    s_tok[tid + 1] = static_cast<int>(sum.tok);
+    s_need[tid + 1] = static_cast<int>(sum.need);
+    s_back[tid + 1] = static_cast<int>(sum.back);
+    s_len[tid] = c.len;
+    if (tid == 0) {
+      s_tok[0] = static_cast<int>(sum.tok) - c.grow;
+      s_need[0] = static_cast<int>(sum.need) - c.need;
+      s_back[0] = static_cast<int>(sum.back) - c.back;
+    }
+    if (tid < n && (i0 + tid) / kThreads % gridDim.x == blockIdx.x)
+      a.starts[i0 + tid] = static_cast<int>(sum.tok) - c.grow;
+    __syncthreads();
+    // pages taken
+    for (int x = s_need[0] + me; x < s_need[n]; x += all) {
+      const int i = find(s_need, n, x);
+      a.table[static_cast<long long>(i0 + i) * a.max_pages + pages_of(s_len[i], a.shift) + x -
+              s_need[i]] = ring_at(x);
+    }
+    // pages given back
+    for (int x = s_back[0] + me; x < s_back[n]; x += all) {
+      const int i = find(s_back, n, x);
+      ring_at(free_pages + x) = a.table[static_cast<long long>(i0 + i) * a.max_pages + x - s_back[i]];
+    }
+    // slots, four to a thread
+    const unsigned tok_end = s_tok[n];  // unsigned: a step past 2^31 - 1 must not wrap
+    for (unsigned u = s_tok[0] / 4 * 4 + 4 * me; u < tok_end; u += 4 * all) {
+      const int t0 = static_cast<int>(u);
+      int slot[4], i = -1, last = -1, page = -1;
+      const int from = max(t0, s_tok[0]), to = s_tok[n] - t0 < 4 ? s_tok[n] : t0 + 4;
+      for (int x = 0; x < 4; ++x) {
+        const int t = t0 + x;
+        if (t < from || x >= to - t0) continue;
+        if (i < 0) i = find(s_tok, n, t);
+        while (t >= s_tok[i + 1]) {
+          ++i;
+          last = -1;
+        }
+        const int pos = s_len[i] + t - s_tok[i], at = pos >> a.shift;
+        if (at != last) {
+          last = at;
+          const int have = pages_of(s_len[i], a.shift);
+          page = at < have ? a.table[static_cast<long long>(i0 + i) * a.max_pages + at]
+                           : ring_at(s_need[i] + at - have);
+        }
+        const bool good = page >= 0 && page < a.num_pages;
+        bad_page = bad_page || !good;
+        slot[x] = good ? (page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
+      }
+      if (to - from == 4 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+        *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+        for (int x = 0; x < 4; ++x)
+          if (t0 + x >= from && x < to - t0) a.slots[t0 + x] = slot[x];
+      }
+    }
+    if (!one_scan) __syncthreads();
   }
+  const int tokens = one_scan ? static_cast<int>(total.tok) : static_cast<int>(before.tok);
+  const long long need = one_scan ? total.need : before.need;
+  const long long back = one_scan ? total.back : before.back;
+  for (unsigned t = tokens + me; t < static_cast<unsigned>(a.max_tokens); t += all)
+    a.slots[t] = -1;
   if (bad_page) atomicExch(a.status, kStatusBadCache);
+
+  cluster_sync();  // every CTA has read the lengths and the ring's state
+  for (int i = me; i < a.nseq; i += all) {
+    const int len = a.lens[i], fresh = a.fresh[i];
+    a.lens_out[i] = fresh < 0 ? 0 : len + fresh;
+  }
+  if (me == 0) {
+    a.starts[a.nseq] = tokens;
+    const int at = head + static_cast<int>(need);
+    a.pool_out[0] = at >= a.num_pages ? at - a.num_pages : at;
+    a.pool_out[1] = static_cast<int>(free_pages - need + back);
+  }
 }
 
 }  // namespace
@@ -168,6 +255,22 @@ extern "C" int xattn_paged_plan(int nseq, int page_size, int num_pages, int max_
   const PlanArgs a = {nseq, page_shift_of(page_size), num_pages, max_pages, max_tokens,
                       lens, fresh, pool, ring, table, lens_out, pool_out, starts, slots,
                       ds->status};
-  plan_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cuda_status(cudaGetLastError());
+  // one CTA for a small step, a cluster as the tokens to map grow
+  const int ctas = max_tokens <= 4 * kThreads && nseq <= 256 ? 1
+                   : max_tokens <= 32 * kThreads             ? 8
+                                                             : kMostCtas;
+  cudaError_t e = cudaFuncSetAttribute(plan_kernel,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, plan_kernel, a));
 }
