@@ -20,6 +20,8 @@
 // cluster barrier that tells that every CTA has read them.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "host.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -180,38 +182,56 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
       const int i = find(s_back, n, x);
       ring_at(free_pages + x) = a.table[static_cast<long long>(i0 + i) * a.max_pages + x - s_back[i]];
     }
-    // slots, four to a thread
-    const unsigned tok_end = s_tok[n];  // unsigned: a step past 2^31 - 1 must not wrap
-    for (unsigned u = s_tok[0] / 4 * 4 + 4 * me; u < tok_end; u += 4 * all) {
-      const int t0 = static_cast<int>(u);
-      int slot[4], i = -1, last = -1, page = -1;
-      const int from = max(t0, s_tok[0]), to = s_tok[n] - t0 < 4 ? s_tok[n] : t0 + 4;
-      for (int x = 0; x < 4; ++x) {
-        const int t = t0 + x;
-        if (t < from || x >= to - t0) continue;
-        if (i < 0) i = find(s_tok, n, t);
-        while (t >= s_tok[i + 1]) {
-          ++i;
-          last = -1;
+    // slots: one to a thread in a step of single tokens, where each is another
+    // page; runs of 4 or 16, with one page id for most, as the tokens grow
+    const int here = s_tok[n] - s_tok[0];
+    auto slots_by = [&](auto span) {
+      constexpr int kSpan = decltype(span)::value;
+      const unsigned end = s_tok[n];  // unsigned: a step past 2^31 - 1 must not wrap
+      for (unsigned u = s_tok[0] / kSpan * kSpan + kSpan * me; u < end; u += kSpan * all) {
+        const int t0 = static_cast<int>(u);
+        const int from = max(s_tok[0] - t0, 0), to = min(s_tok[n] - t0, kSpan);
+        int i = find(s_tok, n, t0 + from), last = -1, page = -1;
+        int slot[kSpan < 4 ? kSpan : 4];
+#pragma unroll 4
+        for (int x = 0; x < kSpan; ++x) {
+          if (x >= from && x < to) {
+            const int t = t0 + x;
+            while (t >= s_tok[i + 1]) {
+              ++i;
+              last = -1;
+            }
+            const int pos = s_len[i] + t - s_tok[i], at = pos >> a.shift;
+            if (at != last) {
+              last = at;
+              const int have = pages_of(s_len[i], a.shift);
+              page = at < have ? a.table[static_cast<long long>(i0 + i) * a.max_pages + at]
+                               : ring_at(s_need[i] + at - have);
+              if (page < 0 || page >= a.num_pages) {
+                bad_page = true;
+                page = -1;
+              }
+            }
+            slot[x % 4] = page < 0 ? -1 : (page << a.shift) + (pos & ((1 << a.shift) - 1));
+          }
+          if (kSpan == 1) {
+            a.slots[t0] = slot[0];
+          } else if (x % 4 == 3) {
+            if (x - 3 >= from && x < to && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+              *reinterpret_cast<int4*>(a.slots + t0 + x - 3) =
+                  make_int4(slot[0], slot[1], slot[2], slot[3]);
+            } else {
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                if (x - 3 + y >= from && x - 3 + y < to) a.slots[t0 + x - 3 + y] = slot[y];
+            }
+          }
         }
-        const int pos = s_len[i] + t - s_tok[i], at = pos >> a.shift;
-        if (at != last) {
-          last = at;
-          const int have = pages_of(s_len[i], a.shift);
-          page = at < have ? a.table[static_cast<long long>(i0 + i) * a.max_pages + at]
-                           : ring_at(s_need[i] + at - have);
-        }
-        const bool good = page >= 0 && page < a.num_pages;
-        bad_page = bad_page || !good;
-        slot[x] = good ? (page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
       }
-      if (to - from == 4 && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
-        *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      } else {
-        for (int x = 0; x < 4; ++x)
-          if (t0 + x >= from && x < to - t0) a.slots[t0 + x] = slot[x];
-      }
-    }
+    };
+    if (here <= all) slots_by(std::integral_constant<int, 1>());
+    else if (here <= 8 * all) slots_by(std::integral_constant<int, 4>());
+    else slots_by(std::integral_constant<int, 16>());
     if (!one_scan) __syncthreads();
   }
   const int tokens = one_scan ? static_cast<int>(total.tok) : static_cast<int>(before.tok);
