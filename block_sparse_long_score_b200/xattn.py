@@ -636,6 +636,39 @@ def xattn_prefill_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
 XATTN_TOKEN_MAJOR, XATTN_HEAD_MAJOR = 0, 1
 
 
+# The paged calls run once or more a layer and token, on kernels of a few
+# microseconds: their checks look at each tensor once, and the device is only
+# switched when it is not the current one.
+
+def _ready(t: torch.Tensor, name: str, device: int, dtype) -> int:
+    """Address of a contiguous tensor of this type on this CUDA device."""
+    if t.get_device() != device or t.dtype is not dtype or not t.is_contiguous():
+        _check(t, name, dtype)
+        raise ValueError(f"every tensor must be on cuda:{device}, got {name} on {t.device}")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return device
+
+
+def _call_on(device: int, fn: str, *args) -> None:
+    """Calls an entry point with the device's current stream as last argument."""
+    f = getattr(_lib_handle or _lib(), fn)
+    # the stream's address alone: torch.cuda.current_stream builds an object, 3 us a call
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if device == torch._C._cuda_getDevice():
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream)
+    if rc != 0:
+        raise XattnError(fn, rc)
+
+
 def make_paged(k_pages: torch.Tensor, hq: int, nseq: int, max_pages: int) -> _Paged:
     """Shape of a paged cache whose pages are ``k_pages`` [num_pages, hkv,
     page_size, d] (any strides with contiguous features)."""
@@ -656,11 +689,12 @@ def make_paged(k_pages: torch.Tensor, hq: int, nseq: int, max_pages: int) -> _Pa
                   hs if hkv > 1 else d, ts)
 
 
-def _paged_pair(k_pages, v_pages, hq: int, nseq: int, max_pages: int) -> _Paged:
+def _paged_pair(k_pages, v_pages, hq: int, nseq: int, max_pages: int, device: int) -> _Paged:
     """Shape of the cache, after checking the V pages against the K pages."""
-    if not (k_pages.is_cuda and v_pages.is_cuda):
-        raise ValueError("the pages must be CUDA tensors")
-    if v_pages.dtype != k_pages.dtype or v_pages.shape != k_pages.shape:
+    if v_pages.get_device() != device or k_pages.get_device() != device:
+        raise ValueError(f"every tensor must be on cuda:{device}, got pages on "
+                         f"{k_pages.device} and {v_pages.device}")
+    if v_pages.dtype is not k_pages.dtype or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have the same type and shape")
     shape = make_paged(k_pages, hq, nseq, max_pages)
     if v_pages.stride() != k_pages.stride():
@@ -681,39 +715,31 @@ def xattn_paged_plan(lens: torch.Tensor, fresh: torch.Tensor, pool: torch.Tensor
     (lens, pool, starts [nseq + 1], slots [max_tokens]) to write to (the first
     two may be the inputs themselves); without it they are allocated, with
     room for ``max_tokens`` slots. Returns (lens, pool, starts, slots)."""
-    for t, n in ((lens, "lens"), (fresh, "fresh"), (pool, "pool"), (ring, "ring"),
-                 (table, "table")):
-        _check(t, n, torch.int32)
+    dev, i32 = _device_of(lens, "lens"), torch.int32
     if lens.dim() != 1 or table.dim() != 2 or ring.dim() != 1:
         raise ValueError("expected lens [nseq], ring [num_pages] and table [nseq, max_pages]")
-    nseq = lens.shape[0]
-    if table.shape[0] != nseq:
+    nseq = lens.numel()
+    if table.size(0) != nseq:
         raise ValueError("table needs a row for each request")
-    _check_shape(fresh, (nseq,), "fresh")
-    _check_shape(pool, (2,), "pool")
+    if fresh.numel() != nseq or pool.numel() != 2:
+        raise ValueError("fresh must be [nseq] and pool [2]")
     if out is None:
         if max_tokens is None:
             raise ValueError("max_tokens is needed when no buffers are given")
         out = (torch.empty_like(lens), torch.empty_like(pool),
-               torch.empty(nseq + 1, device=lens.device, dtype=torch.int32),
-               torch.empty(max_tokens, device=lens.device, dtype=torch.int32))
+               torch.empty(nseq + 1, device=lens.device, dtype=i32),
+               torch.empty(max_tokens, device=lens.device, dtype=i32))
     lens_out, pool_out, starts, slots = out
-    for t, n in ((lens_out, "lens output"), (pool_out, "pool output"), (starts, "starts"),
-                 (slots, "slots")):
-        _check(t, n, torch.int32)
-    _check_shape(lens_out, (nseq,), "lens output")
-    _check_shape(pool_out, (2,), "pool output")
-    _check_shape(starts, (nseq + 1,), "starts")
-    if slots.dim() != 1 or (max_tokens is not None and slots.shape[0] != max_tokens):
+    if lens_out.numel() != nseq or pool_out.numel() != 2 or starts.numel() != nseq + 1:
+        raise ValueError("the outputs must be lens [nseq], pool [2] and starts [nseq + 1]")
+    if slots.dim() != 1 or (max_tokens is not None and slots.numel() != max_tokens):
         raise ValueError("slots must be [max_tokens]")
-    _same_device(lens, fresh, pool, ring, table, lens_out, pool_out, starts, slots)
-    with torch.cuda.device(lens.device):
-        rc = _lib().xattn_paged_plan(
-            nseq, page_size, ring.shape[0], table.shape[1], slots.shape[0], lens.data_ptr(),
-            fresh.data_ptr(), pool.data_ptr(), ring.data_ptr(), table.data_ptr(),
-            lens_out.data_ptr(), pool_out.data_ptr(), starts.data_ptr(), slots.data_ptr(),
-            _stream(lens.device))
-    _raise("xattn_paged_plan", rc)
+    _call_on(dev, "xattn_paged_plan", nseq, page_size, ring.numel(), table.size(1),
+             slots.numel(), _ready(lens, "lens", dev, i32), _ready(fresh, "fresh", dev, i32),
+             _ready(pool, "pool", dev, i32), _ready(ring, "ring", dev, i32),
+             _ready(table, "table", dev, i32), _ready(lens_out, "lens output", dev, i32),
+             _ready(pool_out, "pool output", dev, i32), _ready(starts, "starts", dev, i32),
+             _ready(slots, "slots", dev, i32))
     return out
 
 
@@ -721,9 +747,10 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the tokens of a [tokens, hkv, d] tensor whose tokens
     are contiguous themselves (a slice of a fused projection is one)."""
     n, hkv, d = t.shape
-    if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d):
+    tokens, heads, features = t.stride()
+    if features != 1 or (hkv > 1 and heads != d):
         raise ValueError(f"the [hkv, d] rows of {name} must be contiguous")
-    return t.stride(0) if n > 1 else hkv * d
+    return tokens if n > 1 else hkv * d
 
 
 def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
@@ -735,36 +762,35 @@ def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
     ``starts`` (int32 [nseq + 1]), they are request after request, each a
     contiguous [hkv, L_i, d] array: the packed layout of xattn_prefill_varlen,
     or [batch, hkv, L, d] tensors; they hold len(slots) tokens' rows."""
-    _check(slots, "slots", torch.int32)
+    dev, dtype = _device_of(k_pages, "k_pages"), k_pages.dtype
     if slots.dim() != 1:
         raise ValueError("slots must be [tokens]")
-    if K.dtype != k_pages.dtype or V.dtype != k_pages.dtype:
+    if K.dtype is not dtype or V.dtype is not dtype:
         raise ValueError("K, V and the pages must have one type")
-    tokens, nseq = slots.shape[0], 1
+    tokens, nseq, stride, first = slots.numel(), 1, 0, None
     if starts is None:
-        if K.dim() != 3 or K.shape != (tokens,) + (k_pages.shape[1], k_pages.shape[3]) \
-                or V.shape != K.shape:
+        like = (tokens, k_pages.size(1), k_pages.size(3))
+        if K.shape != like or V.shape != like:
             raise ValueError("without starts, K and V must be [len(slots), hkv, d]")
         stride = _token_stride(K, "K")
-        if _token_stride(V, "V") != stride:
+        if V.stride() != K.stride() and _token_stride(V, "V") != stride:
             raise ValueError("K and V must have the same token stride")
+        if K.get_device() != dev or V.get_device() != dev:
+            raise ValueError(f"every tensor must be on cuda:{dev}, got K on {K.device} and V "
+                             f"on {V.device}")
     else:
-        _check(K, "K")
-        _check(V, "V")
-        _check(starts, "starts", torch.int32)
-        nseq, stride = starts.numel() - 1, 0
-        rows = tokens * k_pages.shape[1] * k_pages.shape[3]
+        _ready(K, "K", dev, dtype)
+        _ready(V, "V", dev, dtype)
+        first = _ready(starts, "starts", dev, torch.int32)
+        nseq = starts.numel() - 1
+        rows = tokens * k_pages.size(1) * k_pages.size(3)
         if nseq < 1 or K.numel() != rows or V.numel() != rows:
             raise ValueError("with starts, K and V must hold len(slots) * hkv rows of d")
-    shape = _paged_pair(k_pages, v_pages, 1, nseq, 1)
-    _same_device(k_pages, K, V, slots, starts, v_pages)
-    with torch.cuda.device(k_pages.device):
-        rc = _lib().xattn_paged_append(
-            K.data_ptr(), V.data_ptr(), ctypes.byref(shape), tokens,
-            XATTN_TOKEN_MAJOR if starts is None else XATTN_HEAD_MAJOR, stride,
-            slots.data_ptr(), None if starts is None else starts.data_ptr(), k_pages.data_ptr(),
-            v_pages.data_ptr(), _stream(k_pages.device))
-    _raise("xattn_paged_append", rc)
+    shape = _paged_pair(k_pages, v_pages, 1, nseq, 1, dev)
+    _call_on(dev, "xattn_paged_append", K.data_ptr(), V.data_ptr(), ctypes.byref(shape), tokens,
+             XATTN_TOKEN_MAJOR if starts is None else XATTN_HEAD_MAJOR, stride,
+             _ready(slots, "slots", dev, torch.int32), first, k_pages.data_ptr(),
+             v_pages.data_ptr())
 
 
 def xattn_paged_decode_workspace_bytes(shape: _Paged) -> int:
@@ -780,43 +806,37 @@ def xattn_paged_decode(Q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     [nseq, hq, d] (or [nseq, hq, 1, d]); pages [num_pages, hkv, page_size, d];
     table int32 [nseq, max_pages]; lens int32 [nseq]. Returns O like Q, or (O,
     lse [nseq, hq]) if lse is True or a tensor."""
-    _check(Q, "Q", k_pages.dtype)
-    _check(table, "table", torch.int32)
-    _check(lens, "lens", torch.int32)
-    if Q.dim() < 3 or Q.numel() != Q.shape[0] * Q.shape[1] * Q.shape[-1]:
+    dev, dtype = _device_of(Q, "Q"), k_pages.dtype
+    if Q.dim() < 3 or Q.numel() != Q.size(0) * Q.size(1) * Q.size(-1):
         raise ValueError("Q must be [nseq, hq, d] or [nseq, hq, 1, d]")
-    nseq, hq = Q.shape[0], Q.shape[1]
-    if table.dim() != 2 or table.shape[0] != nseq:
+    nseq, hq = Q.size(0), Q.size(1)
+    if table.dim() != 2 or table.size(0) != nseq:
         raise ValueError("table must be [nseq, max_pages]")
-    _check_shape(lens, (nseq,), "lens")
-    shape = _paged_pair(k_pages, v_pages, hq, nseq, table.shape[1])
-    if Q.shape[-1] != shape.d:
+    if lens.numel() != nseq:
+        raise ValueError("lens must be [nseq]")
+    shape = _paged_pair(k_pages, v_pages, hq, nseq, table.size(1), dev)
+    if Q.size(-1) != shape.d:
         raise ValueError("Q and the pages must have the same head size")
     if out is None:
         out = torch.empty_like(Q)
-    else:
-        _check(out, "O", Q.dtype)
-        _check_shape(out, Q.shape, "O")
-    want_lse = lse is not None and lse is not False
-    if lse is True:
+    elif out.shape != Q.shape:
+        raise ValueError(f"O must have shape {tuple(Q.shape)}, got {tuple(out.shape)}")
+    if lse is False:
+        lse = None
+    elif lse is True:
         lse = torch.empty(nseq, hq, device=Q.device, dtype=torch.float32)
-    elif want_lse:
-        _check(lse, "lse", torch.float32)
-        _check_shape(lse, (nseq, hq), "lse")
+    elif lse is not None and lse.shape != (nseq, hq):
+        raise ValueError(f"lse must have shape {(nseq, hq)}, got {tuple(lse.shape)}")
     if workspace is None:
         workspace = torch.empty(max(xattn_paged_decode_workspace_bytes(shape), 1),
                                 device=Q.device, dtype=torch.uint8)
-    else:
-        _check(workspace, "workspace")
-    _same_device(Q, k_pages, v_pages, table, lens, out, lse if want_lse else None, workspace)
-    with torch.cuda.device(Q.device):
-        rc = _lib().xattn_paged_decode(
-            Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ctypes.byref(shape),
-            table.data_ptr(), lens.data_ptr(), out.data_ptr(),
-            lse.data_ptr() if want_lse else None, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(Q.device))
-    _raise("xattn_paged_decode", rc)
-    return (out, lse) if want_lse else out
+    _call_on(dev, "xattn_paged_decode", _ready(Q, "Q", dev, dtype), k_pages.data_ptr(),
+             v_pages.data_ptr(), ctypes.byref(shape), _ready(table, "table", dev, torch.int32),
+             _ready(lens, "lens", dev, torch.int32), _ready(out, "O", dev, dtype),
+             None if lse is None else _ready(lse, "lse", dev, torch.float32),
+             _ready(workspace, "workspace", dev, workspace.dtype),
+             workspace.numel() * workspace.element_size())
+    return out if lse is None else (out, lse)
 
 
 def xattn_selftest_timeout(device=None) -> None:
