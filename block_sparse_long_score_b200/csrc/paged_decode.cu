@@ -7,16 +7,23 @@
 // against 4 * g * d flops, g flops a byte in bf16 (26 TFLOP/s at the measured
 // copy rate for g = 4).
 //
-// Work split. The tokens of every (request, KV head) are cut into tiles of
-// kWarps * kChunk tokens, all tiles are numbered in a row, and each CTA takes an
-// equal range of them, whatever the lengths: one long request and many ragged
-// ones load the GPU alike. A CTA walks the (request, head) units of its
-// range. A unit inside one CTA's range is written straight to O; one that
-// several CTAs share leaves a partial result (running maximum, sum,
-// unnormalised o) in the workspace, at most two a CTA, and a second kernel,
-// launched with programmatic stream serialization, joins them in CTA order.
-// The ranges are worked out on the device from lens, so a captured graph
-// follows the lengths.
+// Work split. A unit is a request's KV head; its tokens are cut into tiles of
+// kWarps * kChunk. Two ways, chosen on the host by what the table can hold:
+//  * Ranges. The tiles of all units are numbered in a row and each CTA takes an
+//    equal range of them, whatever the lengths: one long request and many
+//    ragged ones load the GPU alike. A unit inside one CTA's range is written
+//    straight to O; one that several CTAs share leaves a partial result
+//    (running maximum, sum, unnormalised o) in the workspace, at most two a
+//    CTA, and a second kernel, launched with programmatic stream
+//    serialization, joins them in CTA order.
+//  * Units. Each unit goes to a CTA, or to a cluster of CTAs whose results meet
+//    through distributed shared memory: one launch, no scan of the lengths and
+//    no workspace. For many more units than the GPU has room for, which the
+//    block scheduler balances (256 requests of up to 500 tokens, 8 KV heads:
+//    66.4 us in ranges), and for tables of so few tokens that latency is all
+//    (one request of 517 tokens: 10.5 us in ranges).
+// Both work the bounds out on the device from lens, so a captured graph follows
+// the lengths.
 //
 // Inside a CTA the warps take the tile's chunks, each with its own running
 // maximum, sum and o; they meet once at the end of a unit. A warp's K and V come
@@ -49,7 +56,8 @@ struct Split {
 struct DecodeArgs {
   PagedDims D;
   int hc, per;  // chunks the group's heads are cut into, and heads in a chunk
-  bool by_unit; // Split entries are indexed by unit
+  bool by_unit;  // Split entries are indexed by unit
+  int cluster;   // CTAs a unit (the split by units)
   const void *Q, *k_pages, *v_pages;
   const int32_t *table, *lens;
   void* O;
@@ -512,119 +520,71 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float x, float y) {
   *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
 }
 
-// First tile of CTA group b's range: total * b / groups.
-__device__ __forceinline__ unsigned long long range_of(unsigned long long total, int b,
-                                                       int groups) {
-  return total * static_cast<unsigned>(b) / static_cast<unsigned>(groups);
+// Part of a unit that a CTA has.
+struct Unit {
+  unsigned left;  // tiles of the CTA's range from this unit's first on
+  int request, len, head, t0, steps;  // t0: its first tile here; steps: tiles here
+};
+
+// A cluster's shared memory: this address in CTA `rank` of it.
+__device__ __forceinline__ const float4* in_cluster(const float4* p, int rank) {
+  unsigned long long r;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+  return reinterpret_cast<const float4*>(r);
 }
 
 // O = 0 and lse = -inf for the requests that hold nothing.
 template <class Core>
+__device__ __forceinline__ void empty_row(const DecodeArgs& a, int request, int head, int head0,
+                                          int heads) {
+  constexpr int kHalf = Core::kDim / 2;
+  const long long row = static_cast<long long>(request) * a.D.hq + head * a.D.group + head0;
+  for (int x = threadIdx.x; x < heads * kHalf; x += kWarps * 32) {
+    store_pair(static_cast<typename Core::T*>(a.O) + row * Core::kDim + 2 * x, 0.0f, 0.0f);
+    if (x % kHalf == 0 && a.lse != nullptr) a.lse[row + x / kHalf] = -INFINITY;
+  }
+}
+template <class Core>
 __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part, int head0,
                            int heads) {
-  constexpr int kHalf = Core::kDim / 2;
-  const PagedDims& D = a.D;
-  for (int i = group; i < D.nseq; i += groups) {
+  for (int i = group; i < a.D.nseq; i += groups) {
     if (clamped(a, a.lens[i]) != 0) continue;
-    for (int x = threadIdx.x; x < D.hkv * heads * kHalf; x += kWarps * 32) {
-      const int h = x / kHalf, head = h / heads;
-      const long long row =
-          static_cast<long long>(i) * D.hq + head * D.group + head0 + h % heads;
-      store_pair(static_cast<typename Core::T*>(a.O) + row * Core::kDim + x % kHalf * 2, 0.0f,
-                 0.0f);
-      if (x % kHalf == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
-      if (a.by_unit && x % (heads * kHalf) == 0) split_of(a, i, head, part)->more = 0;
+    for (int head = 0; head < a.D.hkv; ++head) {
+      empty_row<Core>(a, i, head, head0, heads);
+      if (a.by_unit && threadIdx.x == 0) split_of(a, i, head, part)->more = 0;
     }
   }
 }
 
-template <class Core>
+template <class Core, bool kUnits>
 __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using T = typename Core::T;
   constexpr int kTile = kWarps * Core::kChunk, kThreads = kWarps * 32;
+  constexpr int kStages = stages_of<Core>();
   const PagedDims& D = a.D;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  // CTAs b * hc .. b * hc + hc - 1 take the same tiles for different heads of
-  // the group, at about the same time: the second to read a row finds it in L2.
-  const int part = blockIdx.x % a.hc, group = blockIdx.x / a.hc;
-  int groups = gridDim.x / a.hc;
+  // CTAs (clusters) b * hc .. b * hc + hc - 1 take the same tiles for different
+  // heads of the group, at about the same time: the second to read a row finds
+  // it in L2.
+  const int block = kUnits ? blockIdx.x / a.cluster : blockIdx.x;
+  const int part = block % a.hc, group = block / a.hc;
   const int head0 = part * a.per, heads = min(a.per, D.group - head0);
 
-  constexpr int kStages = stages_of<Core>();
   extern __shared__ char s_dynamic[];
   __shared__ uint64_t s_full[kWarps][kStages];
   __shared__ int s_abort;
-  __shared__ unsigned long long s_sum[kWarps], s_before;
-  __shared__ int s_request, s_len;
 
-  asm volatile("griddepcontrol.launch_dependents;");
   if (lane < kStages) mbar_init(&s_full[warp][lane], 1);
   if (tid == 0) s_abort = 0;
   fence_barrier_init();  // a warp's barriers are used by its own lanes and the TMA unit
 
-  // Where this CTA's range begins: a scan of the requests' tile counts, a run
-  // of requests to each thread.
-  const int run = (D.nseq + kThreads - 1) / kThreads;
-  const int i0 = min(tid * run, D.nseq), i1 = min(i0 + run, D.nseq);
-  unsigned long long mine = 0;
-  bool bad = false, empty = false;
-  for (int i = i0; i < i1; ++i) {
-    const int raw = a.lens[i], n = clamped(a, raw);
-    bad = bad || n != raw;
-    empty = empty || n == 0;
-    mine += (n + kTile - 1) / kTile;
-  }
-  if (bad && blockIdx.x == 0) atomicExch(a.status, kStatusBadCache);
-  unsigned long long upto = mine;
-  for (int x = 1; x < 32; x *= 2) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, x);
-    if (lane >= x) upto += y;
-  }
-  if (lane == 31) s_sum[warp] = upto;
-  empty = __syncthreads_or(empty);
-  unsigned long long total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += s_sum[w];
-    total += s_sum[w];
-  }
-  total *= D.hkv;
-  if (empty) empty_rows<Core>(a, group, groups, part, head0, heads);
-  if (!a.by_unit && tid == 0) a.split[blockIdx.x].more = 0;
-  // as many ranges as there are tiles, at most: none is empty, so a unit's
-  // partial results are those of consecutive CTAs
-  groups = static_cast<int>(min(static_cast<unsigned long long>(groups), total));
-  if (group >= groups) return;
-  unsigned long long pos = range_of(total, group, groups);
-  const unsigned long long end = range_of(total, group + 1, groups);
-  unsigned long long before = (upto - mine) * D.hkv;
-  if (pos >= before && pos < upto * D.hkv) {
-    for (int i = i0; i < i1; ++i) {
-      const int n = clamped(a, a.lens[i]);
-      const unsigned long long next =
-          before + static_cast<unsigned long long>((n + kTile - 1) / kTile) * D.hkv;
-      if (pos < next) {
-        s_request = i;
-        s_len = n;
-        s_before = before;
-        break;
-      }
-      before = next;
-    }
-  }
-  __syncthreads();
-  // The units of the range in turn. Two of these walk it: one issues copies, the
-  // other, some stages behind, uses them.
-  struct Unit {
-    unsigned long long left;  // tiles of the range from this unit's first on
-    int request, len, head, t0, steps;
-  };
-  auto steps_of = [&](const Unit& u) {
-    const int tiles = (u.len + kTile - 1) / kTile;
-    return static_cast<int>(min(static_cast<unsigned long long>(tiles - u.t0), u.left));
-  };
-  auto next_unit = [&](Unit& u) {  // u.left > u.steps
+  // The part of the first unit that is this CTA's.
+  Unit use;
+  bool bad = false;
+  [[maybe_unused]] unsigned total = 0, end = 0, groups = 0;  // of the split into ranges
+  auto next_unit = [&](Unit& u) {  // within the range: u.left > u.steps
     u.left -= u.steps;
     u.t0 = 0;
     if (++u.head == D.hkv) {
@@ -632,18 +592,95 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       do u.len = clamped(a, a.lens[++u.request]);
       while (u.len == 0);
     }
-    u.steps = steps_of(u);
+    u.steps = static_cast<int>(min(static_cast<unsigned>((u.len + kTile - 1) / kTile), u.left));
   };
-  Unit use;
-  use.left = end - pos;
-  use.request = s_request;
-  use.len = s_len;
-  {
-    const int tiles = (use.len + kTile - 1) / kTile;
+  if constexpr (kUnits) {
+    const int rank = blockIdx.x % a.cluster;
+    use.request = group / D.hkv;
+    use.head = group % D.hkv;
+    const int raw = a.lens[use.request];
+    use.len = clamped(a, raw);
+    if (use.len != raw && rank == 0 && tid == 0) atomicExch(a.status, kStatusBadCache);
+    if (use.len == 0) {  // so for the whole cluster
+      if (rank == 0) empty_row<Core>(a, use.request, use.head, head0, heads);
+      return;
+    }
+    const unsigned tiles = (use.len + kTile - 1) / kTile;
+    use.t0 = static_cast<int>(static_cast<unsigned long long>(tiles) * rank / a.cluster);
+    use.steps =
+        static_cast<int>(static_cast<unsigned long long>(tiles) * (rank + 1) / a.cluster) - use.t0;
+    use.left = use.steps;
+    __syncthreads();
+  } else {
+    __shared__ unsigned s_sum[kWarps], s_before;
+    __shared__ int s_request, s_len;
+    asm volatile("griddepcontrol.launch_dependents;");
+    // Where the range begins: a scan of the requests' tile counts, a run of
+    // requests to each thread. (The host has made sure of fewer than 2^31 tiles.)
+    const int launched = gridDim.x / a.hc;
+    const int run = (D.nseq + kThreads - 1) / kThreads;
+    const int i0 = min(tid * run, D.nseq), i1 = min(i0 + run, D.nseq);
+    unsigned mine = 0;
+    int len = 0;
+    bool empty = false;
+    for (int i = i0; i < i1; ++i) {
+      const int raw = a.lens[i];
+      len = clamped(a, raw);
+      bad = bad || len != raw;
+      empty = empty || len == 0;
+      mine += (len + kTile - 1) / kTile;
+    }
+    if (bad && blockIdx.x == 0) atomicExch(a.status, kStatusBadCache);
+    bad = false;
+    unsigned upto = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += y;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    empty = __syncthreads_or(empty);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += s_sum[w];
+      total += s_sum[w];
+    }
+    total *= D.hkv;
+    if (empty) empty_rows<Core>(a, group, launched, part, head0, heads);
+    if (!a.by_unit && tid == 0) a.split[blockIdx.x].more = 0;
+    // as many ranges as there are tiles, at most: none is empty, so a unit's
+    // partial results are those of consecutive CTAs
+    groups = min(static_cast<unsigned>(launched), total);
+    if (group >= static_cast<int>(groups)) return;
+    // range b begins at total * b / groups
+    const unsigned each = total / groups, over = total % groups;
+    const unsigned pos = group * each + group * over / groups;
+    end = (group + 1) * each + (group + 1) * over / groups;
+    unsigned before = (upto - mine) * D.hkv;
+    if (pos >= before && pos < upto * D.hkv) {
+      for (int i = i0; i < i1; ++i) {
+        if (run > 1) len = clamped(a, a.lens[i]);
+        const unsigned next = before + static_cast<unsigned>((len + kTile - 1) / kTile) * D.hkv;
+        if (pos < next) {
+          s_request = i;
+          s_len = len;
+          s_before = before;
+          break;
+        }
+        before = next;
+      }
+    }
+    __syncthreads();
+    use.left = end - pos;
+    use.request = s_request;
+    use.len = s_len;
+    const unsigned tiles = (use.len + kTile - 1) / kTile;
     use.head = static_cast<int>((pos - s_before) / tiles);
     use.t0 = static_cast<int>((pos - s_before) % tiles);
+    use.steps = static_cast<int>(min(tiles - use.t0, use.left));
   }
-  use.steps = steps_of(use);
+  // Two of these walk the range's units: one issues copies, the other, some
+  // stages behind, uses them.
   Unit ahead = use;
 
   Core core;
@@ -651,7 +688,6 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   char* rings = s_dynamic + (1024 - smem_u32(s_dynamic) % 1024) % 1024;
   char* ring = rings + warp * kStages * Core::kStage;
   float4* bufs = reinterpret_cast<float4*>(rings + kWarps * kStages * Core::kStage);
-  bad = false;
 
   // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
   int step = 0, pages = -1, pages_next = -1;
@@ -667,7 +703,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   pages = page_batch(0);
   pages_next = page_batch(32);
   uint32_t valids = 0;  // rows of the chunks under way, 5 bits each, the newest lowest
-  bool done = false;
+  bool done = use.steps == 0;  // (a CTA of a cluster may have none)
   // Copies the warp's next chunk to a stage.
   auto issue = [&](int stage) {
     int valid = 0;
@@ -691,7 +727,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
         }
       }
       if (++step == ahead.steps) {
-        done = ahead.left == static_cast<unsigned long long>(ahead.steps);
+        done = ahead.left == static_cast<unsigned>(ahead.steps);
         if (!done) {
           next_unit(ahead);
           step = 0;
@@ -750,19 +786,39 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       __syncthreads();
       if (warp == 0) core.merge(other_buf, x);
     }
-    if (warp == 0) {
-      core.emit(a, q_row, heads, use.t0 == 0 && use.steps == tiles,
-                blockIdx.x * 2ll + (use.t0 == 0 ? 1 : 0));
-      if (lane == 0 && use.t0 == 0 && (a.by_unit || use.steps < tiles)) {
-        // the group of CTAs whose range holds the unit's last tile
-        const unsigned long long last = end - use.left + tiles - 1;
-        const int to = static_cast<int>(((last + 1) * groups - 1) / total);
-        *split_of(a, use.request, use.head, part) = {use.request, use.head,
-                                                     static_cast<int>(blockIdx.x), to - group};
+    if constexpr (kUnits) {
+      if (a.cluster > 1) {  // the CTAs' results, joined by the first in order of rank
+        const int rank = blockIdx.x % a.cluster;
+        static_assert(Core::kParts <= 2, "the join's two buffers hold a CTA's result");
+        if (warp == 0 && rank > 0)
+#pragma unroll
+          for (int x = 0; x < Core::kParts; ++x) core.put(bufs + x * (Core::kBuf / 16), x);
+        cluster_sync();
+        if (warp == 0 && rank == 0)
+#pragma unroll 1
+          for (int src = 1; src < a.cluster; ++src)
+#pragma unroll
+            for (int x = 0; x < Core::kParts; ++x)
+              core.merge(in_cluster(bufs + x * (Core::kBuf / 16), src), x);
+        cluster_sync();  // no CTA ends while its buffers are read
+        if (rank > 0) break;
       }
+      if (warp == 0) core.emit(a, q_row, heads, true, 0);
+      break;
+    } else {
+      if (warp == 0) {
+        core.emit(a, q_row, heads, use.steps == tiles, blockIdx.x * 2ll + (use.t0 == 0 ? 1 : 0));
+        if (lane == 0 && use.t0 == 0 && (a.by_unit || use.steps < tiles)) {
+          // the group of CTAs whose range holds the unit's last tile
+          const unsigned long long past = end - use.left + tiles;
+          const int to = static_cast<int>((past * groups - 1) / total);
+          *split_of(a, use.request, use.head, part) = {use.request, use.head,
+                                                       static_cast<int>(blockIdx.x), to - group};
+        }
+      }
+      if (use.left == static_cast<unsigned>(use.steps)) break;
+      next_unit(use);
     }
-    if (use.left == static_cast<unsigned long long>(use.steps)) break;
-    next_unit(use);
   }
   if (bad) atomicExch(a.status, kStatusBadCache);
   if (lost && lane == 0) atomicExch(a.status, kStatusTimeout);
@@ -851,33 +907,54 @@ template <class Core>
 cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   constexpr int kTile = kWarps * Core::kChunk;
   const PagedDims& D = a.D;
-  // no more groups than tiles there can be
-  const long long row_tiles = ((static_cast<long long>(D.max_pages) << D.page_shift) + kTile - 1) / kTile;
-  const long long tiles = row_tiles * D.nseq * D.hkv;
-  long long groups = min(static_cast<long long>(num_sms) * Core::kCtas, static_cast<long long>(kMaxCtas)) / a.hc;
-  groups = max(1ll, min(groups, tiles));
-  const unsigned grid = static_cast<unsigned>(groups * a.hc);
+  const long long slots = min(num_sms * Core::kCtas, kMaxCtas);  // CTAs the GPU holds
   const long long units = static_cast<long long>(D.nseq) * D.hkv * a.hc;
-  a.by_unit = units < grid;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_of<Core>());
-  if (e != cudaSuccess) return e;
+  const long long row_tiles =
+      ((static_cast<long long>(D.max_pages) << D.page_shift) + kTile - 1) / kTile;
+  const long long tiles = row_tiles * D.nseq * D.hkv;
   CUtensorMap k_map, v_map;
   if (make_pages_map(&k_map, a.k_pages, D, Core::kBox, Core::kChunk) != XATTN_OK ||
       make_pages_map(&v_map, a.v_pages, D, Core::kBox, Core::kChunk) != XATTN_OK)
     return cudaErrorInvalidValue;
-  decode_kernel<Core><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || row_tiles == 1) return e;  // a unit of one tile is never shared
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.by_unit ? static_cast<unsigned>(units) : grid, a.per);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
+
+  // By units: four waves of them balance themselves; fewer where the table holds
+  // so little that a unit's CTA, or each of its cluster, has eight tiles at most.
+  a.cluster = 1;
+  while (a.cluster < 8 && a.cluster < row_tiles && 2 * a.cluster * units <= slots) a.cluster *= 2;
+  if (units >= 4 * slots || row_tiles <= 8 * a.cluster || tiles >= 1ll << 31) {
+    if (units >= 4 * slots || tiles >= 1ll << 31) a.cluster = 1;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, true>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem_of<Core>());
+    if (e != cudaSuccess) return e;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = a.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
+    cfg.dynamicSmemBytes = smem_of<Core>();
+    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<Core, true>, a, k_map, v_map);
+  }
+
+  // By ranges, no more than there can be tiles.
+  const unsigned grid = static_cast<unsigned>(max(1ll, min(slots / a.hc, tiles)) * a.hc);
+  a.by_unit = units < grid;
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_of<Core>());
+  if (e != cudaSuccess) return e;
+  decode_kernel<Core, false><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.by_unit ? static_cast<unsigned>(units) : grid, a.per);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, join_kernel<typename Core::T, Core::kDim>, a);
 }
@@ -928,7 +1005,7 @@ int xattn_paged_decode(const void* Q, const void* k_pages, const void* v_pages,
   const Cut cut = cut_of(D);
   const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * cut.per;
   char* w = static_cast<char*>(ws);
-  DecodeArgs a = {D, cut.hc, cut.per, false, Q, k_pages, v_pages, table, lens, O, lse, ds->status};
+  DecodeArgs a = {D, cut.hc, cut.per, false, 1, Q, k_pages, v_pages, table, lens, O, lse, ds->status};
   a.split = reinterpret_cast<Split*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + align256(kMaxCtas * sizeof(Split)));
   a.part_o = reinterpret_cast<float*>(w + align256(kMaxCtas * sizeof(Split)) +
