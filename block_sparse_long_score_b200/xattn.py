@@ -669,18 +669,19 @@ def _call_on(device: int, fn: str, *args) -> None:
         raise XattnError(fn, rc)
 
 
+_PAGED_TYPES = {torch.bfloat16: XATTN_BF16, torch.float32: XATTN_F32}
+
+
 def make_paged(k_pages: torch.Tensor, hq: int, nseq: int, max_pages: int) -> _Paged:
     """Shape of a paged cache whose pages are ``k_pages`` [num_pages, hkv,
     page_size, d] (any strides with contiguous features)."""
-    if k_pages.dim() != 4:
+    shape = k_pages.shape
+    if len(shape) != 4:
         raise ValueError("pages must be [num_pages, hkv, page_size, d]")
-    num_pages, hkv, page, d = k_pages.shape
-    if k_pages.dtype == torch.bfloat16:
-        dt = XATTN_BF16
-    elif k_pages.dtype == torch.float32:
-        dt = XATTN_F32
-    else:
+    dt = _PAGED_TYPES.get(k_pages.dtype)
+    if dt is None:
         raise ValueError(f"pages must be bfloat16 or float32, got {k_pages.dtype}")
+    num_pages, hkv, page, d = shape
     ps, hs, ts, es = k_pages.stride()
     if es != 1:
         raise ValueError("the features of a page's row must be contiguous")
@@ -763,13 +764,14 @@ def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
     contiguous [hkv, L_i, d] array: the packed layout of xattn_prefill_varlen,
     or [batch, hkv, L, d] tensors; they hold len(slots) tokens' rows."""
     dev, dtype = _device_of(k_pages, "k_pages"), k_pages.dtype
-    if slots.dim() != 1:
-        raise ValueError("slots must be [tokens]")
+    s_shape, p_shape = slots.shape, k_pages.shape
+    if len(s_shape) != 1 or len(p_shape) != 4:
+        raise ValueError("expected slots [tokens] and pages [num_pages, hkv, page_size, d]")
     if K.dtype is not dtype or V.dtype is not dtype:
         raise ValueError("K, V and the pages must have one type")
-    tokens, nseq, stride, first = slots.numel(), 1, 0, None
+    tokens, nseq, stride, first = s_shape[0], 1, 0, None
     if starts is None:
-        like = (tokens, k_pages.size(1), k_pages.size(3))
+        like = (tokens, p_shape[1], p_shape[3])
         if K.shape != like or V.shape != like:
             raise ValueError("without starts, K and V must be [len(slots), hkv, d]")
         stride = _token_stride(K, "K")
@@ -783,7 +785,7 @@ def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
         _ready(V, "V", dev, dtype)
         first = _ready(starts, "starts", dev, torch.int32)
         nseq = starts.numel() - 1
-        rows = tokens * k_pages.size(1) * k_pages.size(3)
+        rows = tokens * p_shape[1] * p_shape[3]
         if nseq < 1 or K.numel() != rows or V.numel() != rows:
             raise ValueError("with starts, K and V must hold len(slots) * hkv rows of d")
     shape = _paged_pair(k_pages, v_pages, 1, nseq, 1, dev)
@@ -806,21 +808,21 @@ def xattn_paged_decode(Q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     [nseq, hq, d] (or [nseq, hq, 1, d]); pages [num_pages, hkv, page_size, d];
     table int32 [nseq, max_pages]; lens int32 [nseq]. Returns O like Q, or (O,
     lse [nseq, hq]) if lse is True or a tensor."""
-    dev, dtype = _device_of(Q, "Q"), k_pages.dtype
-    if Q.dim() < 3 or Q.numel() != Q.size(0) * Q.size(1) * Q.size(-1):
+    dev, dtype, q_shape, t_shape = _device_of(Q, "Q"), k_pages.dtype, Q.shape, table.shape
+    if len(q_shape) != 3 and (len(q_shape) != 4 or q_shape[2] != 1):
         raise ValueError("Q must be [nseq, hq, d] or [nseq, hq, 1, d]")
-    nseq, hq = Q.size(0), Q.size(1)
-    if table.dim() != 2 or table.size(0) != nseq:
+    nseq, hq = q_shape[0], q_shape[1]
+    if len(t_shape) != 2 or t_shape[0] != nseq:
         raise ValueError("table must be [nseq, max_pages]")
     if lens.numel() != nseq:
         raise ValueError("lens must be [nseq]")
-    shape = _paged_pair(k_pages, v_pages, hq, nseq, table.size(1), dev)
-    if Q.size(-1) != shape.d:
+    shape = _paged_pair(k_pages, v_pages, hq, nseq, t_shape[1], dev)
+    if q_shape[-1] != shape.d:
         raise ValueError("Q and the pages must have the same head size")
     if out is None:
         out = torch.empty_like(Q)
-    elif out.shape != Q.shape:
-        raise ValueError(f"O must have shape {tuple(Q.shape)}, got {tuple(out.shape)}")
+    elif out.shape != q_shape:
+        raise ValueError(f"O must have shape {tuple(q_shape)}, got {tuple(out.shape)}")
     if lse is False:
         lse = None
     elif lse is True:
@@ -834,8 +836,7 @@ def xattn_paged_decode(Q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
              v_pages.data_ptr(), ctypes.byref(shape), _ready(table, "table", dev, torch.int32),
              _ready(lens, "lens", dev, torch.int32), _ready(out, "O", dev, dtype),
              None if lse is None else _ready(lse, "lse", dev, torch.float32),
-             _ready(workspace, "workspace", dev, workspace.dtype),
-             workspace.numel() * workspace.element_size())
+             _ready(workspace, "workspace", dev, workspace.dtype), workspace.nbytes)
     return out if lse is None else (out, lse)
 
 
