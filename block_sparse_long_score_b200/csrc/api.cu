@@ -165,21 +165,24 @@ int make_map_reshaped(CUtensorMap* m, const void* ptr, int S, int R, int bh, int
   return r == CUDA_SUCCESS ? XATTN_OK : XATTN_ERR_CUDA;
 }
 
-// 4-D view [num_pages][hkv][page][d] of a paged cache's K or V, with boxes of
-// box_d features x box_tokens tokens of one page and head; boxes of 128-byte
-// rows of bf16 are swizzled.
+// 5-D view [num_pages][hkv][slice][page][box_d] of a paged cache's K or V, a row's
+// d features cut into slices of box_d, with boxes of box_tokens tokens of one page
+// and head, slice after slice; slices of 128 bytes of bf16 are swizzled.
 int make_pages_map(CUtensorMap* m, const void* ptr, const PagedDims& D, int box_d,
                    int box_tokens) {
   const bool bf16 = D.dtype == XATTN_BF16;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D.d), static_cast<cuuint64_t>(D.page),
+  const cuuint32_t slices = static_cast<cuuint32_t>(D.d / box_d);
+  cuuint64_t dims[5] = {static_cast<cuuint64_t>(box_d), static_cast<cuuint64_t>(D.page), slices,
                         static_cast<cuuint64_t>(D.hkv), static_cast<cuuint64_t>(D.num_pages)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(D.token_stride) * D.esize,
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(D.token_stride) * D.esize,
+                           static_cast<cuuint64_t>(box_d) * D.esize,
                            static_cast<cuuint64_t>(D.head_stride) * D.esize,
                            static_cast<cuuint64_t>(D.page_stride) * D.esize};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), static_cast<cuuint32_t>(box_tokens), 1, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
+  cuuint32_t box[5] = {static_cast<cuuint32_t>(box_d), static_cast<cuuint32_t>(box_tokens), slices,
+                       1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
   CUresult r = g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                        4, const_cast<void*>(ptr), dims, strides, box, es,
+                        5, const_cast<void*>(ptr), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE,
                         bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -58,6 +58,7 @@ struct DecodeArgs {
   int hc, per;  // chunks the group's heads are cut into, and heads in a chunk
   bool by_unit;  // Split entries are indexed by unit
   int cluster;   // CTAs a unit (the split by units)
+  int sms;
   const void *Q, *k_pages, *v_pages;
   const int32_t *table, *lens;
   void* O;
@@ -511,7 +512,19 @@ template <class Core>
 constexpr int smem_of() {
   return 1024 + kWarps * stages_of<Core>() * Core::kStage + 2 * Core::kBuf;
 }
+
 // ------------------------------------------------------------ both kernels
+
+// A chunk's rows, all slices (see make_pages_map).
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int token, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(token), "r"(head),
+      "r"(page)
+      : "memory");
+}
 
 __device__ __forceinline__ void store_pair(float* p, float x, float y) {
   *reinterpret_cast<float2*>(p) = make_float2(x, y);
@@ -649,8 +662,11 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     if (empty) empty_rows<Core>(a, group, launched, part, head0, heads);
     if (!a.by_unit && tid == 0) a.split[blockIdx.x].more = 0;
     // as many ranges as there are tiles, at most: none is empty, so a unit's
-    // partial results are those of consecutive CTAs
-    groups = min(static_cast<unsigned>(launched), total);
+    // partial results are those of consecutive CTAs; and where there are few
+    // tiles, four to a CTA rather than fewer to more of them, with more results
+    // to join (one request of 8192 tokens: 18.5 us with 444 CTAs, 15.5 with 256)
+    groups = min(static_cast<unsigned>(launched),
+                 max(total / 4, min(total, static_cast<unsigned>(a.sms))));
     if (group >= static_cast<int>(groups)) return;
     // range b begins at total * b / groups
     const unsigned each = total / groups, over = total % groups;
@@ -717,13 +733,8 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
           uint64_t* full = &s_full[warp][stage];
           char* to = ring + stage * Core::kStage;
           mbar_arrive_expect_tx(full, Core::kStage);
-#pragma unroll
-          for (int x = 0; x < Core::kDim; x += Core::kBox) {
-            const int at = x * Core::kChunk * static_cast<int>(sizeof(T));
-            tma_load_4d(to + at, &k_map, full, x, t & (D.page - 1), ahead.head, page);
-            tma_load_4d(to + Core::kStage / 2 + at, &v_map, full, x, t & (D.page - 1), ahead.head,
-                        page);
-          }
+          tma_load_5d(to, &k_map, full, t & (D.page - 1), ahead.head, page);
+          tma_load_5d(to + Core::kStage / 2, &v_map, full, t & (D.page - 1), ahead.head, page);
         }
       }
       if (++step == ahead.steps) {
@@ -907,6 +918,7 @@ template <class Core>
 cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   constexpr int kTile = kWarps * Core::kChunk;
   const PagedDims& D = a.D;
+  a.sms = num_sms;
   const long long slots = min(num_sms * Core::kCtas, kMaxCtas);  // CTAs the GPU holds
   const long long units = static_cast<long long>(D.nseq) * D.hkv * a.hc;
   const long long row_tiles =
@@ -1005,7 +1017,7 @@ int xattn_paged_decode(const void* Q, const void* k_pages, const void* v_pages,
   const Cut cut = cut_of(D);
   const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * cut.per;
   char* w = static_cast<char*>(ws);
-  DecodeArgs a = {D, cut.hc, cut.per, false, 1, Q, k_pages, v_pages, table, lens, O, lse, ds->status};
+  DecodeArgs a = {D, cut.hc, cut.per, false, 1, 0, Q, k_pages, v_pages, table, lens, O, lse, ds->status};
   a.split = reinterpret_cast<Split*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + align256(kMaxCtas * sizeof(Split)));
   a.part_o = reinterpret_cast<float*>(w + align256(kMaxCtas * sizeof(Split)) +
