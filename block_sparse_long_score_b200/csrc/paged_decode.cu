@@ -130,13 +130,19 @@ struct CoreBf16 {
   static constexpr int kChunk = 16;          // tokens of a warp's step
   static constexpr int kBox = 64;            // features of a TMA box: 128 bytes
   // three CTAs an SM with two 8 KB stages a warp, or two with three
-  static constexpr int kCtas = NT == 1 ? 3 : 2, kRing = NT == 1 ? 16384 : 24576;
+  static constexpr int kCtas = NT <= 2 ? 3 : 2, kRing = NT <= 2 ? 16384 : 24576;
   static constexpr int kStage = 2 * kChunk * kD * 2;   // K, then V, box after box
   static constexpr int kParts = NT;                  // a warp's result is joined in parts
   static constexpr int kBuf = (kD / 16 + 1) * 512;   // of this size
   using T = __nv_bfloat16;
 
-  uint32_t q[NT][kD / 8], p[NT][2];
+  // Q: in registers for up to 8 heads. For more it would take half of them, and
+  // sits in shared memory, swizzled like K.
+  static constexpr bool kQShared = NT > 1;
+  static constexpr int kQBytes = kQShared ? 8 * NT * kD * 2 : 0;
+  static constexpr int kQEach = kQShared ? kQBytes / 16 / (kWarps * 32) : 1;
+  uint4 fetched[kQEach];
+  uint32_t q[NT][kQShared ? 1 : kD / 8], q_at, p[NT][2];
   float o[NT][kD / 16][4], m[NT][2], base[NT][2], l[NT][2];
   int r, c;
   // This lane's row of the four 8x8 matrices of an ldmatrix, at the first 16
@@ -152,42 +158,75 @@ struct CoreBf16 {
     v_at = (lane % 8 + lane / 16 * 8) * 128 + ((lane / 8 % 2 ^ lane % 8) << 4);
   }
 
-  // Heads of the unit; rows past the chunk's heads are zero.
-  __device__ __forceinline__ void start(const DecodeArgs& a, long long q_row, int heads) {
+  // Reads the unit's Q (rows past the chunk's heads are zero); `settle` puts it
+  // where the products take it from, and begins the sums.
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, long long q_row, int heads) {
+    if constexpr (kQShared) {  // shared out over the CTA's threads
+#pragma unroll
+      for (int x = 0; x < kQEach; ++x) {
+        const int h = (x * kWarps * 32 + threadIdx.x) / (kD / 8), piece = threadIdx.x % (kD / 8);
+        fetched[x] = h < heads ? static_cast<const uint4*>(a.Q)[(q_row + h) * (kD / 8) + piece]
+                               : make_uint4(0, 0, 0, 0);
+      }
+    } else {
+      const uint32_t* x = static_cast<const uint32_t*>(a.Q) + (q_row + r) * (kD / 2) + c;
+#pragma unroll
+      for (int j = 0; j < kD / 8; ++j) q[0][j] = r < heads ? x[4 * j] : 0;
+    }
+  }
+  __device__ __forceinline__ void settle(char* q_shared) {
+    if constexpr (kQShared) {
+#pragma unroll
+      for (int x = 0; x < kQEach; ++x) {
+        const int h = (x * kWarps * 32 + threadIdx.x) / (kD / 8), piece = threadIdx.x % (kD / 8);
+        *reinterpret_cast<uint4*>(q_shared + h * (kD * 2) + ((piece ^ h % 8) << 4)) = fetched[x];
+      }
+      // ldmatrix: features vary over all four matrices, 32 at a time
+      const uint32_t lane = threadIdx.x % 32;
+      q_at = smem_u32(q_shared) + lane % 8 * (kD * 2) + ((lane / 8 ^ lane % 8) << 4);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const uint32_t* x = static_cast<const uint32_t*>(a.Q) + (q_row + 8 * t + r) * (kD / 2) + c;
-#pragma unroll
-      for (int j = 0; j < kD / 8; ++j) q[t][j] = 8 * t + r < heads ? x[4 * j] : 0;
 #pragma unroll
       for (int i = 0; i < kD / 16; ++i)
 #pragma unroll
-        for (int x4 = 0; x4 < 4; ++x4) o[t][i][x4] = 0.0f;
+        for (int x = 0; x < 4; ++x) o[t][i][x] = 0.0f;
 #pragma unroll
-      for (int x2 = 0; x2 < 2; ++x2) m[t][x2] = -INFINITY, base[t][x2] = 0.0f, l[t][x2] = 0.0f;
+      for (int x = 0; x < 2; ++x) m[t][x] = -INFINITY, base[t][x] = 0.0f, l[t][x] = 0.0f;
     }
   }
 
   __device__ __forceinline__ void scores(uint32_t stage, int valid) {
     const float scale = kLog2e * (kD == 64 ? 0.125f : 0.08838834764831845f);  // log2(e) / sqrt(d)
-    // even and odd steps of 16 features sum apart: two chains half as long
-    float s[NT][4], s1[NT][4];
+    // with few heads, even and odd steps of 16 features sum apart: chains half as long
+    float s[NT][4], s1[1][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[t][j] = s1[t][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) s[t][j] = s1[0][j] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kD / 16; ++i) {
-      uint32_t k[4];
-      ldmatrix(stage + i / 4 * (kChunk * 128) + (k_at ^ i % 4 * 32), k);
+    for (int i = 0; i < kD / 16; i += 2) {
+      uint32_t k0[4], k1[4];
+      ldmatrix(stage + i / 4 * (kChunk * 128) + (k_at ^ i % 4 * 32), k0);
+      ldmatrix(stage + i / 4 * (kChunk * 128) + (k_at ^ (i + 1) % 4 * 32), k1);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        mma_bf16(i % 2 ? s1[t] : s[t], k[0], k[1], k[2], k[3], q[t][2 * i], q[t][2 * i + 1]);
+      for (int t = 0; t < NT; ++t) {
+        uint32_t y[4];
+        if constexpr (kQShared) {
+          // features 16 i .. + 31: pieces 2 i .. + 3, xor'ed with the head in their low 3 bits
+          ldmatrix((q_at ^ i % 4 * 32) + i / 4 * 128 + t * (8 * kD * 2), y);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = q[t][2 * i + j];
+        }
+        mma_bf16(s[t], k0[0], k0[1], k0[2], k0[3], y[0], y[1]);
+        mma_bf16(NT == 1 ? s1[0] : s[t], k1[0], k1[1], k1[2], k1[3], y[2], y[3]);
+      }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[t][j] = (s[t][j] + s1[t][j]) * scale;
+      for (int j = 0; j < 4; ++j) s[t][j] = (NT == 1 ? s[t][j] + s1[0][j] : s[t][j]) * scale;
       if (valid < kChunk) {
         if (r >= valid) s[t][0] = s[t][1] = -INFINITY;
         if (r + 8 >= valid) s[t][2] = s[t][3] = -INFINITY;
@@ -347,14 +386,23 @@ struct CoreF32 {
     g = threadIdx.x % 32 / 8;
     c = threadIdx.x % 8;
   }
-  __device__ __forceinline__ void start(const DecodeArgs& a, long long q_row, int heads) {
-    const float scale = kLog2e / sqrtf(static_cast<float>(kD));
+  static constexpr bool kQShared = false;
+  static constexpr int kQBytes = 0;
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, long long q_row, int heads) {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       const float* p = static_cast<const float*>(a.Q) + (q_row + h) * kD + c * 4;
 #pragma unroll
+      for (int j = 0; j < kPer; ++j) q[h][j] = h < heads ? p[j / 4 * 32 + j % 4] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void settle(char*) {
+    const float scale = kLog2e / sqrtf(static_cast<float>(kD));
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        q[h][j] = h < heads ? p[j / 4 * 32 + j % 4] * scale : 0.0f;
+        q[h][j] *= scale;
         o[h][j] = 0.0f;
       }
       m[h] = -INFINITY;
@@ -507,10 +555,11 @@ constexpr int stages_of() {
   return Core::kRing / Core::kStage < 6 ? Core::kRing / Core::kStage : 6;
 }
 // Shared memory of a CTA: the warps' rings (on 1024-byte boundaries, as the
-// swizzle wants them), then two buffers of the join.
+// swizzle wants them), then two buffers of the join; the second is also Q's.
 template <class Core>
 constexpr int smem_of() {
-  return 1024 + kWarps * stages_of<Core>() * Core::kStage + 2 * Core::kBuf;
+  return 1024 + kWarps * stages_of<Core>() * Core::kStage + Core::kBuf +
+         (Core::kBuf > Core::kQBytes ? Core::kBuf : Core::kQBytes);
 }
 
 // ------------------------------------------------------------ both kernels
@@ -705,6 +754,12 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   char* ring = rings + warp * kStages * Core::kStage;
   float4* bufs = reinterpret_cast<float4*>(rings + kWarps * kStages * Core::kStage);
 
+  // Q before the copies, whose bytes it would queue behind
+  auto q_row_of = [&](const Unit& u) {
+    return static_cast<long long>(u.request) * D.hq + u.head * D.group + head0;
+  };
+  core.fetch(a, q_row_of(use), heads);
+
   // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
   int step = 0, pages = -1, pages_next = -1;
   auto page_batch = [&](int step0) {
@@ -758,10 +813,8 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   uint32_t phases = 0;  // parity of each stage's next wait
   bool lost = false;    // a wait ran out
   while (true) {
-    const int tiles = (use.len + kTile - 1) / kTile;
-    const long long q_row =
-        static_cast<long long>(use.request) * D.hq + use.head * D.group + head0;
-    core.start(a, q_row, heads);
+    core.settle(reinterpret_cast<char*>(bufs + Core::kBuf / 16));
+    if constexpr (Core::kQShared) __syncthreads();
 #pragma unroll 1
     for (int x = 0; x < use.steps; ++x) {
       const int valid = static_cast<int>(valids >> (5 * (kStages - 1)) & 31);
@@ -784,9 +837,18 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
+    const Unit was = use;
+    const long long q_row = q_row_of(was);
+    const bool last = was.left == static_cast<unsigned>(was.steps);
+    if (!last) {  // the next unit's Q, while this one's results are joined
+      next_unit(use);
+      core.fetch(a, q_row_of(use), heads);
+    }
+
     // the warps' results of this unit, joined in a fixed order: 0 + 2, 1 + 3, then both
-    float4* mine_buf = bufs + warp % 2 * (Core::kBuf / 16);
-    float4* other_buf = bufs + Core::kBuf / 16;
+    // (warp 1's buffer is read last, and is not the one that takes the next unit's Q)
+    float4* mine_buf = bufs + (1 - warp % 2) * (Core::kBuf / 16);
+    float4* other_buf = bufs;
 #pragma unroll
     for (int x = 0; x < Core::kParts; ++x) {
       __syncthreads();
@@ -800,17 +862,18 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     if constexpr (kUnits) {
       if (a.cluster > 1) {  // the CTAs' results, joined by the first in order of rank
         const int rank = blockIdx.x % a.cluster;
-        static_assert(Core::kParts <= 2, "the join's two buffers hold a CTA's result");
+        static_assert(Core::kParts * Core::kBuf <= kWarps * kStages * Core::kStage, "ring");
+        float4* all = reinterpret_cast<float4*>(rings);  // every copy has been used
         if (warp == 0 && rank > 0)
 #pragma unroll
-          for (int x = 0; x < Core::kParts; ++x) core.put(bufs + x * (Core::kBuf / 16), x);
+          for (int x = 0; x < Core::kParts; ++x) core.put(all + x * (Core::kBuf / 16), x);
         cluster_sync();
         if (warp == 0 && rank == 0)
 #pragma unroll 1
           for (int src = 1; src < a.cluster; ++src)
 #pragma unroll
             for (int x = 0; x < Core::kParts; ++x)
-              core.merge(in_cluster(bufs + x * (Core::kBuf / 16), src), x);
+              core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x);
         cluster_sync();  // no CTA ends while its buffers are read
         if (rank > 0) break;
       }
@@ -818,17 +881,17 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       break;
     } else {
       if (warp == 0) {
-        core.emit(a, q_row, heads, use.steps == tiles, blockIdx.x * 2ll + (use.t0 == 0 ? 1 : 0));
-        if (lane == 0 && use.t0 == 0 && (a.by_unit || use.steps < tiles)) {
+        const int tiles = (was.len + kTile - 1) / kTile;
+        core.emit(a, q_row, heads, was.steps == tiles, blockIdx.x * 2ll + (was.t0 == 0 ? 1 : 0));
+        if (lane == 0 && was.t0 == 0 && (a.by_unit || was.steps < tiles)) {
           // the group of CTAs whose range holds the unit's last tile
-          const unsigned long long past = end - use.left + tiles;
+          const unsigned long long past = end - was.left + tiles;
           const int to = static_cast<int>((past * groups - 1) / total);
-          *split_of(a, use.request, use.head, part) = {use.request, use.head,
+          *split_of(a, was.request, was.head, part) = {was.request, was.head,
                                                        static_cast<int>(blockIdx.x), to - group};
         }
       }
-      if (use.left == static_cast<unsigned>(use.steps)) break;
-      next_unit(use);
+      if (last) break;
     }
   }
   if (bad) atomicExch(a.status, kStatusBadCache);
@@ -907,7 +970,7 @@ struct Cut {
   int hc, per;
 };
 Cut cut_of(const PagedDims& D) {
-  const int most = D.dtype == XATTN_BF16 ? 16 : 4;
+  const int most = D.dtype == XATTN_BF16 ? 32 : 4;
   const int hc = (D.group + most - 1) / most;
   return {hc, (D.group + hc - 1) / hc};
 }
@@ -973,8 +1036,9 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
 
 template <int kD>
 cudaError_t launch_bf16(const DecodeArgs& a, int num_sms, cudaStream_t st) {
-  return a.per <= 8 ? launch_decode<CoreBf16<kD, 1>>(a, num_sms, st)
-                    : launch_decode<CoreBf16<kD, 2>>(a, num_sms, st);
+  return a.per <= 8    ? launch_decode<CoreBf16<kD, 1>>(a, num_sms, st)
+         : a.per <= 16 ? launch_decode<CoreBf16<kD, 2>>(a, num_sms, st)
+                       : launch_decode<CoreBf16<kD, 4>>(a, num_sms, st);
 }
 
 template <int kD>
