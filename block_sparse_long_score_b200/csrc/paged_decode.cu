@@ -129,8 +129,11 @@ struct CoreBf16 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 16;          // tokens of a warp's step
   static constexpr int kBox = 64;            // features of a TMA box: 128 bytes
-  // three CTAs an SM with two 8 KB stages a warp, or two with three
-  static constexpr int kCtas = NT <= 2 ? 3 : 2, kRing = NT <= 2 ? 16384 : 24576;
+  // CTAs an SM, and bytes of a warp's ring: 96 or 128 KB of copies under way an
+  // SM. With 192 KB every page id and Q row queues 4 us behind them, and DRAM is
+  // no faster (24 KB rings against 16: one 128K request 91.4 against 86.9 us, two
+  // of 76800 tokens without shared heads 200.4 against 193.6).
+  static constexpr int kCtas = kD == 128 ? 2 : 3, kRing = kD == 128 ? 16384 : 8192;
   static constexpr int kStage = 2 * kChunk * kD * 2;   // K, then V, box after box
   static constexpr int kParts = NT;                  // a warp's result is joined in parts
   static constexpr int kBuf = (kD / 16 + 1) * 512;   // of this size
@@ -370,7 +373,7 @@ struct CoreF32 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 8;
   static constexpr int kBox = kD;
-  static constexpr int kCtas = H == 4 ? 2 : 3, kRing = H == 4 ? 24576 : 16384;
+  static constexpr int kCtas = kD == 128 ? 2 : H == 4 ? 4 : 3, kRing = kD == 128 ? 16384 : 8192;
   static constexpr int kPieces = kD / 32;
   static constexpr int kStage = 2 * kChunk * kD * 4;
   static constexpr int kPart = H < 2 ? 1 : 2;  // heads joined at a time
@@ -549,7 +552,7 @@ struct CoreF32 {
   }
 };
 
-// Stages of a warp's ring: kRing bytes a warp where the stages are that large.
+// Stages of a warp's ring.
 template <class Core>
 constexpr int stages_of() {
   return Core::kRing / Core::kStage < 6 ? Core::kRing / Core::kStage : 6;
