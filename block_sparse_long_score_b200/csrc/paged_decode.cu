@@ -309,7 +309,7 @@ struct CoreBf16 {
       buf[i * 32] = make_float4(o[t][i][0], o[t][i][1], o[t][i][2], o[t][i][3]);
     buf[kD / 16 * 32] = make_float4(m[t][0], m[t][1], l[t][0], l[t][1]);
   }
-  __device__ __forceinline__ void merge(const float4* buf, int t) {
+  __device__ __forceinline__ void merge(const float4* buf, int t, int) {
     buf += threadIdx.x % 32;
     const float4 ml = buf[kD / 16 * 32];
     rescale(t, 0, ml.x);
@@ -367,165 +367,209 @@ struct CoreBf16 {
 // ------------------------------------------------------------ fp32 core
 // CUDA cores: no tensor-core type keeps fp32's mantissa. A warp's chunk is 8
 // tokens, two (g, g + 4) to each group g of 8 lanes; of every 32 features lane c
-// of a group holds 4 c .. + 3, so a group reads 128 contiguous bytes at a time.
+// of a group holds 4 c .. + 3, so a group reads 128 contiguous bytes at a time,
+// and multiplies two features an instruction (f32x2). The 2 H dot products of a
+// group are summed over its lanes by halves (a lane keeps one half of the
+// values at each step and hands on the other), which takes 14 exchanges in
+// place of 48 for 8 heads and leaves each logit with one owner: of head h and
+// token g + 4 t it is lane (2 h + t) * 8 / (2 H) of the group, or the lane of the
+// head for 8 heads, with both tokens. So a weight's exponential is taken once, and
+// handed to the group. (16 requests of up to 16384 tokens, 16 heads a KV head of 64:
+// 69.9 us; with a sum for every lane, FMAs of one feature and passes of 4 heads 88.7.)
 template <int kD, int H>
 struct CoreF32 {
   static constexpr int kDim = kD;
   static constexpr int kChunk = 8;
   static constexpr int kBox = kD;
-  static constexpr int kCtas = kD == 128 ? 2 : H == 4 ? 4 : 3, kRing = kD == 128 ? 16384 : 8192;
+  static constexpr int kCtas = kD * H >= 512 || kD == 128 ? 2 : 3, kRing = kD == 128 ? 16384 : 8192;
   static constexpr int kPieces = kD / 32;
   static constexpr int kStage = 2 * kChunk * kD * 4;
   static constexpr int kPart = H < 2 ? 1 : 2;  // heads joined at a time
   static constexpr int kParts = H / kPart;
   static constexpr int kBuf = (kPart * kPieces + 1) * 512;
+  static constexpr bool kQShared = false;
+  static constexpr int kQBytes = 0;
   using T = float;
-  static constexpr int kPer = kD / 8;
+  using F2 = unsigned long long;               // two floats
+  static constexpr int kPairs = kD / 16;       // a lane's of one row
+  static constexpr int kOwn = H == 8 ? 2 : 1;  // logits a lane owns, of one head
 
-  float q[H][kPer], o[H][kPer], m[H], base[H], l[H], w[2][H];
+  F2 q[H][kPairs], o[H][kPairs];
+  float m, base, l;         // of the lane's head (l: its own weights only)
+  float w[kOwn], fs[2], fo[2];
   int g, c;
 
   __device__ __forceinline__ void init() {
     g = threadIdx.x % 32 / 8;
     c = threadIdx.x % 8;
   }
-  static constexpr bool kQShared = false;
-  static constexpr int kQBytes = 0;
+  // This group's lane that owns the logit of head h and its token t.
+  __device__ __forceinline__ int owner(int h, int t) const {
+    return g * 8 + (H == 8 ? h : (2 * h + t) * (4 / H));
+  }
+  // The sum of a value over the lanes that own logits of one head.
+  __device__ __forceinline__ float over_tokens(float x) const {
+    if (H < 8) x += __shfl_xor_sync(0xffffffffu, x, 4 / H);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+  }
+
   __device__ __forceinline__ void fetch(const DecodeArgs& a, long long q_row, int heads) {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const float* p = static_cast<const float*>(a.Q) + (q_row + h) * kD + c * 4;
+      const ulonglong2* p = reinterpret_cast<const ulonglong2*>(
+                                static_cast<const float*>(a.Q) + (q_row + h) * kD) + c;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) q[h][j] = h < heads ? p[j / 4 * 32 + j % 4] : 0.0f;
+      for (int j = 0; j < kPieces; ++j) {
+        const ulonglong2 y = h < heads ? p[8 * j] : make_ulonglong2(0, 0);
+        q[h][2 * j] = y.x;
+        q[h][2 * j + 1] = y.y;
+      }
     }
   }
   __device__ __forceinline__ void settle(char*) {
     const float scale = kLog2e / sqrtf(static_cast<float>(kD));
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        q[h][j] *= scale;
-        o[h][j] = 0.0f;
+      for (int j = 0; j < kPairs; ++j) {
+        q[h][j] = f2_fma(q[h][j], f2_pack(scale, scale), 0);
+        o[h][j] = 0;
       }
-      m[h] = -INFINITY;
-      base[h] = 0.0f;
-      l[h] = 0.0f;
-    }
+    m = -INFINITY;
+    base = 0.0f;
+    l = 0.0f;
   }
-  __device__ __forceinline__ void read_rows(uint32_t rows, float (&x)[2][kPer]) const {
+  __device__ __forceinline__ void read_rows(uint32_t rows, F2 (&x)[2][kPairs]) const {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
         read16(rows + (g + 4 * t) * (kD * 4) + j * 128 + c * 16,
-               reinterpret_cast<uint32_t*>(&x[t][4 * j]));
+               reinterpret_cast<uint32_t*>(&x[t][2 * j]));
   }
   __device__ __forceinline__ void scores(uint32_t stage, int valid) {
-    float k[2][kPer], s[2][H];
+    F2 k[2][kPairs];
+    float s[2 * H];  // of head h and token t at 2 h + t
     read_rows(stage, k);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        float x = 0.0f;
+      for (int t = 0; t < 2; ++t) {
+        F2 x = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) x = fmaf(q[h][j], k[t][j], x);
-        s[t][h] = x;
+        for (int j = 0; j < kPairs; ++j) x = f2_fma(q[h][j], k[t][j], x);
+        float lo, hi;
+        f2_unpack(x, lo, hi);
+        s[2 * h + t] = lo + hi;
       }
+    int n = 2 * H;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int mask = 4; mask > 0; mask /= 2) {
+      if (n > 1) {
+        n /= 2;
+        const bool upper = (c & mask) != 0;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        s[t][h] += __shfl_xor_sync(0xffffffffu, s[t][h], 1);
-        s[t][h] += __shfl_xor_sync(0xffffffffu, s[t][h], 2);
-        s[t][h] += __shfl_xor_sync(0xffffffffu, s[t][h], 4);
-        if (g + 4 * t >= valid) s[t][h] = -INFINITY;
-      }
-    bool grow = false;  // as in the bf16 core
-#pragma unroll
-    for (int h = 0; h < H; ++h) grow = grow || fmaxf(s[0][h], s[1][h]) > m[h] + 8.0f;
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        float top = fmaxf(s[0][h], s[1][h]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        rescale(h, top);
+        for (int i = 0; i < H; ++i) {
+          if (i >= n) break;
+          const float keep = upper ? s[i + n] : s[i], pass = upper ? s[i] : s[i + n];
+          s[i] = keep + __shfl_xor_sync(0xffffffffu, pass, mask);
+        }
+      } else {
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], mask);
       }
     }
+    // the lane's tokens: both of the group, or that of its place
+    if (valid < kChunk) {
+      const int t = H == 8 ? 0 : c / (4 / H) % 2;
+      if (g + 4 * t >= valid) s[0] = -INFINITY;
+      if (kOwn == 2 && g + 4 >= valid) s[kOwn - 1] = -INFINITY;
+    }
+    float top = kOwn == 2 ? fmaxf(s[0], s[kOwn - 1]) : s[0];
+    if (__any_sync(0xffffffffu, top > m + 8.0f)) {  // as in the bf16 core
+      if (H < 8) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4 / H));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      top = fmaxf(top, m);
+      base = top == -INFINITY ? 0.0f : top;
+      const float f = ex2(m - base);
+      m = top;
+      l *= f;
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      w[0][h] = ex2(s[0][h] - base[h]);
-      w[1][h] = ex2(s[1][h] - base[h]);
-      l[h] += w[0][h] + w[1][h];
+      for (int h = 0; h < H; ++h) scale_head(h, __shfl_sync(0xffffffffu, f, owner(h, 0)));
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      w[i] = ex2(s[i] - base);
+      l += w[i];
     }
   }
-  __device__ __forceinline__ void rescale(int h, float top) {
-    top = fmaxf(top, m[h]);
-    base[h] = top == -INFINITY ? 0.0f : top;
-    const float f = ex2(m[h] - base[h]);
-    m[h] = top;
-    l[h] *= f;
+  __device__ __forceinline__ void scale_head(int h, float f) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) o[h][j] *= f;
+    for (int j = 0; j < kPairs; ++j) o[h][j] = f2_fma(o[h][j], f2_pack(f, f), 0);
   }
   __device__ __forceinline__ void values(uint32_t stage, int valid) {
-    float v[2][kPer];
+    F2 v[2][kPairs];
     read_rows(stage + kStage / 2, v);
     if (valid < kChunk) {  // a weight of 0 does not undo a NaN or infinity
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (g + 4 * t >= valid)
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) v[t][j] = 0.0f;
+          for (int j = 0; j < kPairs; ++j) v[t][j] = 0;
     }
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        o[h][j] = fmaf(w[1][h], v[1][j], fmaf(w[0][h], v[0][j], o[h][j]));
+      for (int t = 0; t < 2; ++t) {
+        const float x = __shfl_sync(0xffffffffu, w[H == 8 ? t : 0], owner(h, t));
+        const F2 xx = f2_pack(x, x);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) o[h][j] = f2_fma(xx, v[t][j], o[h][j]);
+      }
   }
   __device__ __forceinline__ void put(float4* buf, int part) const {
     buf += threadIdx.x % 32;
-    float2* ml = reinterpret_cast<float2*>(buf + kPart * kPieces * 32);
 #pragma unroll
-    for (int x = 0; x < kPart; ++x) {
-      const int h = part * kPart + x;
+    for (int x = 0; x < kPart; ++x)
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
-        buf[(x * kPieces + j) * 32] =
-            make_float4(o[h][4 * j], o[h][4 * j + 1], o[h][4 * j + 2], o[h][4 * j + 3]);
-      ml[x] = make_float2(m[h], l[h]);
-    }
+        *reinterpret_cast<ulonglong2*>(&buf[(x * kPieces + j) * 32]) =
+            make_ulonglong2(o[part * kPart + x][2 * j], o[part * kPart + x][2 * j + 1]);
+    buf[kPart * kPieces * 32] = make_float4(m, l, 0.0f, 0.0f);
   }
-  __device__ __forceinline__ void merge(const float4* buf, int part) {
+  // `which` of the join's two merges (their factors serve all parts).
+  __device__ __forceinline__ void merge(const float4* buf, int part, int which) {
     buf += threadIdx.x % 32;
-    const float2* mls = reinterpret_cast<const float2*>(buf + kPart * kPieces * 32);
+    if (part == 0) {  // the heads' maxima and sums, all at once
+      const float4 ml = buf[kPart * kPieces * 32];
+      const float top = fmaxf(m, ml.x);
+      base = top == -INFINITY ? 0.0f : top;
+      fs[which] = ex2(m - base);
+      fo[which] = ex2(ml.x - base);
+      m = top;
+      l = l * fs[which] + ml.y * fo[which];
+    }
 #pragma unroll
     for (int x = 0; x < kPart; ++x) {
       const int h = part * kPart + x;
-      const float2 ml = mls[x];
-      rescale(h, ml.x);
-      const float f = ex2(ml.x - base[h]);
-      l[h] += ml.y * f;
+      scale_head(h, __shfl_sync(0xffffffffu, fs[which], owner(h, 0)));
+      const float f = __shfl_sync(0xffffffffu, fo[which], owner(h, 0));
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
-        const float4 y = buf[(x * kPieces + j) * 32];
-        o[h][4 * j] += y.x * f;
-        o[h][4 * j + 1] += y.y * f;
-        o[h][4 * j + 2] += y.z * f;
-        o[h][4 * j + 3] += y.w * f;
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&buf[(x * kPieces + j) * 32]);
+        o[h][2 * j] = f2_fma(y.x, f2_pack(f, f), o[h][2 * j]);
+        o[h][2 * j + 1] = f2_fma(y.y, f2_pack(f, f), o[h][2 * j + 1]);
       }
     }
   }
   __device__ __forceinline__ void emit(const DecodeArgs& a, long long q_row, int heads, bool whole,
                                        long long slot) {
+    const float all = over_tokens(l);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      float sum = l[h];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const float sum = __shfl_sync(0xffffffffu, all, owner(h, 0));
+      const float top = __shfl_sync(0xffffffffu, m, owner(h, 0));
       if (h >= heads) continue;
       const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
       float* out = whole ? static_cast<float*>(a.O) + (q_row + h) * kD
@@ -533,9 +577,10 @@ struct CoreF32 {
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         float x[4];
+        f2_unpack(o[h][2 * j], x[0], x[1]);
+        f2_unpack(o[h][2 * j + 1], x[2], x[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = o[h][4 * j + i];
           x[i] += __shfl_xor_sync(0xffffffffu, x[i], 8);
           x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
         }
@@ -544,9 +589,10 @@ struct CoreF32 {
               make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
       }
       if (threadIdx.x % 32 == 0) {
-        if (!whole) a.part_ml[slot * a.per + h] = make_float2(m[h], sum);
+        if (!whole) a.part_ml[slot * a.per + h] = make_float2(top, sum);
         else if (a.lse != nullptr)
-          a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base[h] * kLn2 + logf(sum);
+          a.lse[q_row + h] =
+              sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(sum);
       }
     }
   }
@@ -857,10 +903,10 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       __syncthreads();
       if (warp >= 2) core.put(mine_buf, x);
       __syncthreads();
-      if (warp < 2) core.merge(mine_buf, x);
+      if (warp < 2) core.merge(mine_buf, x, 0);
       if (warp == 1) core.put(mine_buf, x);
       __syncthreads();
-      if (warp == 0) core.merge(other_buf, x);
+      if (warp == 0) core.merge(other_buf, x, 1);
     }
     if constexpr (kUnits) {
       if (a.cluster > 1) {  // the CTAs' results, joined by the first in order of rank
@@ -876,7 +922,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
           for (int src = 1; src < a.cluster; ++src)
 #pragma unroll
             for (int x = 0; x < Core::kParts; ++x)
-              core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x);
+              core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x, 0);
         cluster_sync();  // no CTA ends while its buffers are read
         if (rank > 0) break;
       }
@@ -973,7 +1019,7 @@ struct Cut {
   int hc, per;
 };
 Cut cut_of(const PagedDims& D) {
-  const int most = D.dtype == XATTN_BF16 ? 32 : 4;
+  const int most = D.dtype == XATTN_BF16 ? 32 : D.d == 128 ? 4 : 8;
   const int hc = (D.group + most - 1) / most;
   return {hc, (D.group + hc - 1) / hc};
 }
@@ -1048,6 +1094,8 @@ template <int kD>
 cudaError_t launch_f32(const DecodeArgs& a, int num_sms, cudaStream_t st) {
   if (a.per == 1) return launch_decode<CoreF32<kD, 1>>(a, num_sms, st);
   if (a.per == 2) return launch_decode<CoreF32<kD, 2>>(a, num_sms, st);
+  if constexpr (kD < 128)
+    if (a.per > 4) return launch_decode<CoreF32<kD, 8>>(a, num_sms, st);
   return launch_decode<CoreF32<kD, 4>>(a, num_sms, st);
 }
 
