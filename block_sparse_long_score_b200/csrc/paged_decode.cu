@@ -947,14 +947,30 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   if (lost && lane == 0) atomicExch(a.status, kStatusTimeout);
 }
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
 
-// Joins the partial results of a unit for one query head (blockIdx.y). The
-// weights 2^(m - max) are worked out for 32 partials at a time, a lane each;
-// then a warp adds every kJoinWarps-th partial's row, in that order.
+__device__ __forceinline__ void store_row(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_row(float* p, const float (&x)[2]) { store_pair(p, x[0], x[1]); }
+__device__ __forceinline__ void store_row(float* p, const float (&x)[1]) { *p = x[0]; }
+__device__ __forceinline__ void load_row(const float* p, float (&x)[4]) {
+  const float4 y = *reinterpret_cast<const float4*>(p);
+  x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+}
+__device__ __forceinline__ void load_row(const float* p, float (&x)[2]) {
+  const float2 y = *reinterpret_cast<const float2*>(p);
+  x[0] = y.x, x[1] = y.y;
+}
+__device__ __forceinline__ void load_row(const float* p, float (&x)[1]) { x[0] = *p; }
+
+// Joins the partial results of a unit for one query head (blockIdx.y). A warp adds
+// every kJoinWarps-th partial's row, in that order; the first rows are read
+// together with the maxima and sums their weights 2^(m - max) come from.
 template <typename T, int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a) {
   constexpr int kPer = kD / 32;  // features a lane
+  constexpr int kAtOnce = 8;     // rows
   __shared__ float s_o[kJoinWarps][kD], s_w[kMaxCtas], s_max[kJoinWarps], s_sum[kJoinWarps];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -962,52 +978,68 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs 
   if (s.more == 0) return;
   const int head0 = s.first % a.hc * a.per;
   if (head0 + h >= a.D.group) return;
-  auto slot_of = [&](int p) {
-    return ((s.first + static_cast<long long>(p) * a.hc) * 2 + (p == 0 ? 1 : 0)) * a.per + h;
-  };
+  const long long step = 2ll * a.hc * a.per;  // partial results between two CTAs of a unit
+  const long long at0 = (2ll * s.first + 1) * a.per + h, at1 = (2ll * s.first) * a.per + h;
+  auto slot_of = [&](int p) { return p == 0 ? at0 : at1 + p * step; };
   const int parts = s.more + 1;
-  float m = -INFINITY;
-  for (int p = tid; p < parts; p += kJoinWarps * 32) m = fmaxf(m, a.part_ml[slot_of(p)].x);
+  float y[kAtOnce][kPer];
+#pragma unroll
+  for (int x = 0; x < kAtOnce; ++x) {
+    const int p = warp + x * kJoinWarps;
+    if (p < parts) load_row(a.part_o + slot_of(p) * kD + lane * kPer, y[x]);
+  }
+  float2 ml = make_float2(-INFINITY, 0.0f);
+  if (tid < parts) ml = a.part_ml[slot_of(tid)];
+  float m = ml.x;
+  for (int p = tid + kJoinWarps * 32; p < parts; p += kJoinWarps * 32)
+    m = fmaxf(m, a.part_ml[slot_of(p)].x);
+#pragma unroll
   for (int x = 16; x > 0; x /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   if (lane == 0) s_max[warp] = m;
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_max[w]);
   const float base = m == -INFINITY ? 0.0f : m;
   float sum = 0.0f;
   for (int p = tid; p < parts; p += kJoinWarps * 32) {
-    const float2 ml = a.part_ml[slot_of(p)];
+    if (p != tid) ml = a.part_ml[slot_of(p)];
     const float w = ex2(ml.x - base);
     s_w[p] = w;
     sum += ml.y * w;
   }
+#pragma unroll
   for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
   float o[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
-#pragma unroll 4
-  for (int p = warp; p < parts; p += kJoinWarps) {
-    const float* row = a.part_o + slot_of(p) * kD + lane;
-    const float w = s_w[p];
+  for (int p0 = warp; p0 < parts; p0 += kAtOnce * kJoinWarps) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) o[j] += row[j * 32] * w;
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int p = p0 + x * kJoinWarps;
+      if (p >= parts) continue;
+      if (p0 != warp) load_row(a.part_o + slot_of(p) * kD + lane * kPer, y[x]);
+      const float w = s_w[p];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o[j] += y[x][j] * w;
+    }
   }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) s_o[warp][j * 32 + lane] = o[j];
+  store_row(&s_o[warp][lane * kPer], o);
   __syncthreads();
   const long long row =
       static_cast<long long>(s.request) * a.D.hq + s.head * a.D.group + head0 + h;
   if (tid >= kD / 2) return;
   sum = 0.0f;
-  float2 y = make_float2(0.0f, 0.0f);
+  float2 z = make_float2(0.0f, 0.0f);
+#pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
     sum += s_sum[w];
-    y.x += s_o[w][2 * tid];
-    y.y += s_o[w][2 * tid + 1];
+    z.x += s_o[w][2 * tid];
+    z.y += s_o[w][2 * tid + 1];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  store_pair(static_cast<T*>(a.O) + row * kD + 2 * tid, y.x * inv, y.y * inv);
+  store_pair(static_cast<T*>(a.O) + row * kD + 2 * tid, z.x * inv, z.y * inv);
   if (tid == 0 && a.lse != nullptr)
     a.lse[row] = sum == 0.0f ? -INFINITY : base * kLn2 + logf(sum);
 }

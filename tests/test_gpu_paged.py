@@ -82,6 +82,53 @@ def test_plan(n, page, longest, kind, in_place):
     assert xattn_get_device_status() == 0
 
 
+def test_large_plan_replays_in_a_graph():
+    """A step whose slots take the second kernel, captured in place and replayed
+    on other lengths, one of them a step that cannot be done."""
+    rng = random.Random(8)
+    n, page, room = 40, 16, 50000
+    lens = torch.zeros(n, dtype=torch.int32, device=DEV)
+    fresh, pool = torch.zeros_like(lens), torch.zeros(2, dtype=torch.int32, device=DEV)
+    state = _plan_state(rng, n, page, 2000, "prefill", spare_pages=900)
+    ring, table = (torch.zeros_like(_i32(x)) for x in state[3:])
+    starts = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    slots = torch.zeros(room, dtype=torch.int32, device=DEV)
+    call = lambda: xattn_paged_plan(lens, fresh, pool, ring, table, page,
+                                    out=(lens, pool, starts, slots))
+    call()                                     # pool says no page is free: nothing to do
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    lack = [list(x) for x in state[:3]] + [state[3], state[4]]
+    lack[2][1] = 10
+    for s, code in ((state, 0), (lack, -6)):
+        want = R.plan(*s, page, room)
+        for dst, src in zip((lens, fresh, pool, ring, table), s):
+            dst.copy_(_i32(src))
+        slots.fill_(CANARY)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, g, w in zip(("lens", "pool", "starts", "slots", "ring", "table"),
+                              (lens, pool, starts, slots, ring, table), want):
+            assert g.tolist() == w, name
+        assert xattn_get_device_status() == code
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_plan_writes_slots_at_any_alignment(offset):
+    state = _plan_state(random.Random(offset), 30, 16, 3000, "prefill")
+    tokens = sum(state[1])
+    t = [_i32(x) for x in state]
+    buf = torch.full((tokens + 9,), CANARY, dtype=torch.int32, device=DEV)
+    out = (torch.empty_like(t[0]), torch.empty_like(t[2]),
+           torch.empty(31, dtype=torch.int32, device=DEV), buf[offset:offset + tokens + 2])
+    xattn_paged_plan(*t, 16, out=out)
+    want = R.plan(*state, 16, tokens + 2)
+    assert out[3].tolist() == want[3]
+    assert bool((buf[:offset] == CANARY).all()) and bool((buf[offset + tokens + 2:] == CANARY).all())
+
+
 @pytest.mark.parametrize("n", [5, 1500])
 @pytest.mark.parametrize("what,code", [("pages", -6), ("tokens", -1), ("row", -1),
                                        ("negative", -1), ("fresh", -1), ("head", -1),
@@ -337,6 +384,62 @@ def test_decode_batches(hq, hkv, d, dtype, page, lens):
 def test_decode_many_requests(n, dtype):
     rng = random.Random(n)
     _check_decode(*_cache([rng.choice((0, 1, 5, 17, 40)) for _ in range(n)], 2, 1, 64, dtype, 16))
+
+
+def _wide(Q, kp, vp, table, lens, columns):
+    """The same requests in a table with room for far more tokens: the work is
+    cut by tile ranges, where a narrow table's goes to CTAs or clusters by unit."""
+    more = torch.full((table.shape[0], columns), 1 << 30, dtype=torch.int32, device=DEV)
+    return Q, kp, vp, torch.cat([table, more], 1), lens
+
+
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [1], [0, 0, 1, 0], [16], [17, 0, 15], [64], [65],
+                                  [128, 1], [300, 64, 0, 129], [1000], [0, 700, 0, 0, 3, 2000],
+                                  list(range(40)), [33] * 70])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F3, 128), (F3, 32)])
+def test_decode_short_requests_in_a_wide_table(lens, dtype, d):
+    _check_decode(*_wide(*_cache(lens, 8, 2, d, dtype, 16, seed=len(lens)), 4000))
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 8, 9, 16, 17, 32, 33, 64, 128])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F3, 128), (F3, 64), (F3, 32)])
+def test_decode_groups_in_a_wide_table(group, dtype, d):
+    """Units shared by several CTAs, for every count of heads a pass serves."""
+    _check_decode(*_wide(*_cache([777, 0, 1500], group, 1, d, dtype, 32, seed=group), 3000))
+
+
+@pytest.mark.parametrize("n", [1, 127, 128, 129, 400])
+def test_decode_scan_of_the_lengths(n):
+    """As many requests as the scan's threads, one less, one more, several each."""
+    rng = random.Random(n)
+    lens = [rng.choice((0, 0, 1, 40, 200)) for _ in range(n)]
+    _check_decode(*_wide(*_cache(lens, 4, 2, 64, BF, 16, seed=n), 2000))
+
+
+def test_decode_narrow_and_wide_tables_agree():
+    """Both ways to cut the work are within the bound of the same fp64 result,
+    and within twice that of each other."""
+    c = _cache([500, 31, 0, 900], 16, 2, 128, BF, 16)
+    a, _ = _check_decode(*c)
+    b, _ = _check_decode(*_wide(*c, 4000))
+    tol = R.decode(*c)[2]
+    assert bool(((a.double() - b.double()).abs().cpu() <= 2 * tol).all())
+
+
+def test_decode_table_of_more_than_2_to_31_entries():
+    """A table whose capacity is past 2^31 tiles and whose last rows lie past
+    2^31 entries: only the entries of the lengths are read."""
+    n, columns = 260, (1 << 31) // 256 - 1
+    Q, kp, vp, table, lens = _cache([0] * (n - 3) + [700, 0, 300], 8, 2, 128, BF, 256)
+    big = torch.empty(n, columns, dtype=torch.int32, device=DEV)
+    assert big.numel() > 1 << 31
+    big[:, :table.shape[1]] = table
+    out, lse = xattn_paged_decode(Q, kp, vp, big, lens, lse=True)
+    torch.cuda.synchronize()
+    assert xattn_get_device_status() == 0
+    O, L, tol, tol_lse = R.decode(Q, kp, vp, table, lens)
+    assert bool(((out.cpu().double() - O).abs() <= tol).all())
+    assert bool((lse[:n - 3].cpu() == -float("inf")).all())
 
 
 @pytest.mark.parametrize("dtype", [BF, F3])
