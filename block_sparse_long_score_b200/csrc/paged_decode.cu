@@ -188,6 +188,9 @@ struct CoreBf16 {
       const uint32_t lane = threadIdx.x % 32;
       q_at = smem_u32(q_shared) + lane % 8 * (kD * 2) + ((lane / 8 ^ lane % 8) << 4);
     }
+    clear();
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -432,10 +435,14 @@ struct CoreF32 {
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        q[h][j] = f2_fma(q[h][j], f2_pack(scale, scale), 0);
-        o[h][j] = 0;
-      }
+      for (int j = 0; j < kPairs; ++j) q[h][j] = f2_fma(q[h][j], f2_pack(scale, scale), 0);
+    clear();
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) o[h][j] = 0;
     m = -INFINITY;
     base = 0.0f;
     l = 0.0f;
@@ -811,17 +818,17 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
 
   // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
   int step = 0, pages = -1, pages_next = -1;
-  auto page_batch = [&](int step0) {
-    const int t = (ahead.t0 + step0 + lane) * kTile + warp * Core::kChunk;
-    if (step0 + lane >= ahead.steps || t >= ahead.len) return -1;
-    const int page = a.table[static_cast<long long>(ahead.request) * D.max_pages +
+  auto page_batch = [&](const Unit& u, int step0) {
+    const int t = (u.t0 + step0 + lane) * kTile + warp * Core::kChunk;
+    if (step0 + lane >= u.steps || t >= u.len) return -1;
+    const int page = a.table[static_cast<long long>(u.request) * D.max_pages +
                              (t >> D.page_shift)];
     if (page >= 0 && page < D.num_pages) return page;
     bad = true;
     return -1;
   };
-  pages = page_batch(0);
-  pages_next = page_batch(32);
+  pages = page_batch(ahead, 0);
+  pages_next = page_batch(ahead, 32);
   uint32_t valids = 0;  // rows of the chunks under way, 5 bits each, the newest lowest
   bool done = use.steps == 0;  // (a CTA of a cluster may have none)
   // Copies the warp's next chunk to a stage.
@@ -846,18 +853,33 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
         if (!done) {
           next_unit(ahead);
           step = 0;
-          pages = page_batch(0);
-          pages_next = page_batch(32);
+          pages = page_batch(ahead, 0);
+          pages_next = page_batch(ahead, 32);
         }
       } else if (step % 32 == 0) {
         pages = pages_next;
-        pages_next = page_batch(step + 32);
+        pages_next = page_batch(ahead, step + 32);
       }
     }
     valids = valids << 5 | static_cast<unsigned>(valid);
   };
   for (int x = 0; x < kStages; ++x) issue(x);
 
+  // The warps' results of a unit, joined in a fixed order: 0 + 2, 1 + 3, then both.
+  // (warp 1's buffer is read last, and is not the one that takes the next unit's Q)
+  auto join_warps = [&]() {
+    float4* mine_buf = bufs + (1 - warp % 2) * (Core::kBuf / 16);
+#pragma unroll
+    for (int x = 0; x < Core::kParts; ++x) {
+      __syncthreads();
+      if (warp >= 2) core.put(mine_buf, x);
+      __syncthreads();
+      if (warp < 2) core.merge(mine_buf, x, 0);
+      if (warp == 1) core.put(mine_buf, x);
+      __syncthreads();
+      if (warp == 0) core.merge(bufs, x, 1);
+    }
+  };
   int stage = 0;
   uint32_t phases = 0;  // parity of each stage's next wait
   bool lost = false;    // a wait ran out
@@ -894,22 +916,11 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       core.fetch(a, q_row_of(use), heads);
     }
 
-    // the warps' results of this unit, joined in a fixed order: 0 + 2, 1 + 3, then both
-    // (warp 1's buffer is read last, and is not the one that takes the next unit's Q)
-    float4* mine_buf = bufs + (1 - warp % 2) * (Core::kBuf / 16);
-    float4* other_buf = bufs;
-#pragma unroll
-    for (int x = 0; x < Core::kParts; ++x) {
-      __syncthreads();
-      if (warp >= 2) core.put(mine_buf, x);
-      __syncthreads();
-      if (warp < 2) core.merge(mine_buf, x, 0);
-      if (warp == 1) core.put(mine_buf, x);
-      __syncthreads();
-      if (warp == 0) core.merge(other_buf, x, 1);
-    }
+    join_warps();
     if constexpr (kUnits) {
-      if (a.cluster > 1) {  // the CTAs' results, joined by the first in order of rank
+      if (a.cluster > 1) {
+        // the CTAs' results: the first CTA's warps take those of two CTAs each, in
+        // order of rank, and join theirs
         const int rank = blockIdx.x % a.cluster;
         static_assert(Core::kParts * Core::kBuf <= kWarps * kStages * Core::kStage, "ring");
         float4* all = reinterpret_cast<float4*>(rings);  // every copy has been used
@@ -917,12 +928,15 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
 #pragma unroll
           for (int x = 0; x < Core::kParts; ++x) core.put(all + x * (Core::kBuf / 16), x);
         cluster_sync();
-        if (warp == 0 && rank == 0)
+        if (rank == 0) {
+          if (warp > 0) core.clear();
 #pragma unroll 1
-          for (int src = 1; src < a.cluster; ++src)
+          for (int src = warp > 0 ? warp : kWarps; src < a.cluster; src += kWarps)
 #pragma unroll
             for (int x = 0; x < Core::kParts; ++x)
               core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x, 0);
+          join_warps();
+        }
         cluster_sync();  // no CTA ends while its buffers are read
         if (rank > 0) break;
       }
