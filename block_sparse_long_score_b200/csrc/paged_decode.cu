@@ -135,7 +135,8 @@ struct CoreBf16 {
   // of 76800 tokens without shared heads 200.4 against 193.6).
   static constexpr int kCtas = kD == 128 ? 2 : 3, kRing = kD == 128 ? 16384 : 8192;
   static constexpr int kStage = 2 * kChunk * kD * 2;   // K, then V, box after box
-  static constexpr int kParts = NT;                  // a warp's result is joined in parts
+  static constexpr int kParts = NT;                  // a warp's result is joined in parts,
+  static constexpr bool kSpread = true;              // each in another warp,
   static constexpr int kBuf = (kD / 16 + 1) * 512;   // of this size
   using T = __nv_bfloat16;
 
@@ -330,38 +331,35 @@ struct CoreBf16 {
     }
   }
 
-  // The unit's result: to O and lse, or as the partial result at `slot`.
+  // Part t of the unit's result: to O and lse, or as the partial result at `slot`.
   __device__ __forceinline__ void emit(const DecodeArgs& a, long long q_row, int heads, bool whole,
-                                       long long slot) {
+                                       long long slot, int t) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int x = 0; x < 2; ++x) {
+      float sum = l[t][x];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int h = 8 * t + 2 * c + x;
+      if (h >= heads) continue;
+      if (whole) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T* out = static_cast<T*>(a.O) + (q_row + h) * kD + r;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float sum = l[t][x];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int h = 8 * t + 2 * c + x;
-        if (h >= heads) continue;
-        if (whole) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          T* out = static_cast<T*>(a.O) + (q_row + h) * kD + r;
-#pragma unroll
-          for (int i = 0; i < kD / 16; ++i) {
-            out[16 * i] = __float2bfloat16_rn(o[t][i][x] * inv);
-            out[16 * i + 8] = __float2bfloat16_rn(o[t][i][x + 2] * inv);
-          }
-          if (r == 0 && a.lse != nullptr)
-            a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base[t][x] * kLn2 + logf(sum);
-        } else {
-          float* out = a.part_o + (slot * a.per + h) * kD + r;
-#pragma unroll
-          for (int i = 0; i < kD / 16; ++i) {
-            out[16 * i] = o[t][i][x];
-            out[16 * i + 8] = o[t][i][x + 2];
-          }
-          if (r == 0) a.part_ml[slot * a.per + h] = make_float2(m[t][x], sum);
+        for (int i = 0; i < kD / 16; ++i) {
+          out[16 * i] = __float2bfloat16_rn(o[t][i][x] * inv);
+          out[16 * i + 8] = __float2bfloat16_rn(o[t][i][x + 2] * inv);
         }
+        if (r == 0 && a.lse != nullptr)
+          a.lse[q_row + h] = sum == 0.0f ? -INFINITY : base[t][x] * kLn2 + logf(sum);
+      } else {
+        float* out = a.part_o + (slot * a.per + h) * kD + r;
+#pragma unroll
+        for (int i = 0; i < kD / 16; ++i) {
+          out[16 * i] = o[t][i][x];
+          out[16 * i + 8] = o[t][i][x + 2];
+        }
+        if (r == 0) a.part_ml[slot * a.per + h] = make_float2(m[t][x], sum);
       }
     }
   }
@@ -389,6 +387,7 @@ struct CoreF32 {
   static constexpr int kStage = 2 * kChunk * kD * 4;
   static constexpr int kPart = H < 2 ? 1 : 2;  // heads joined at a time
   static constexpr int kParts = H / kPart;
+  static constexpr bool kSpread = false;       // (all heads' maxima come with the first)
   static constexpr int kBuf = (kPart * kPieces + 1) * 512;
   static constexpr bool kQShared = false;
   static constexpr int kQBytes = 0;
@@ -571,10 +570,10 @@ struct CoreF32 {
     }
   }
   __device__ __forceinline__ void emit(const DecodeArgs& a, long long q_row, int heads, bool whole,
-                                       long long slot) {
+                                       long long slot, int part) {
     const float all = over_tokens(l);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
+    for (int h = part * kPart; h < (part + 1) * kPart; ++h) {
       const float sum = __shfl_sync(0xffffffffu, all, owner(h, 0));
       const float top = __shfl_sync(0xffffffffu, m, owner(h, 0));
       if (h >= heads) continue;
@@ -865,19 +864,23 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   };
   for (int x = 0; x < kStages; ++x) issue(x);
 
-  // The warps' results of a unit, joined in a fixed order: 0 + 2, 1 + 3, then both.
-  // (warp 1's buffer is read last, and is not the one that takes the next unit's Q)
+  // The warps' results of a unit, joined in a fixed order. Part x ends up in warp
+  // root_of(x), so that several warps can write a unit's heads out: it takes warp
+  // root ^ 2's, warp root ^ 1 takes root ^ 3's, and then root root ^ 1's.
+  // (bufs[0] is read last, and is not the one that takes the next unit's Q)
+  auto root_of = [](int x) { return Core::kSpread ? x % kWarps : 0; };
   auto join_warps = [&]() {
-    float4* mine_buf = bufs + (1 - warp % 2) * (Core::kBuf / 16);
 #pragma unroll
     for (int x = 0; x < Core::kParts; ++x) {
+      const int to_root = warp ^ root_of(x);
+      float4* buf = bufs + (1 - to_root % 2) * (Core::kBuf / 16);
       __syncthreads();
-      if (warp >= 2) core.put(mine_buf, x);
+      if (to_root >= 2) core.put(buf, x);
       __syncthreads();
-      if (warp < 2) core.merge(mine_buf, x, 0);
-      if (warp == 1) core.put(mine_buf, x);
+      if (to_root < 2) core.merge(buf, x, 0);
+      if (to_root == 1) core.put(buf, x);
       __syncthreads();
-      if (warp == 0) core.merge(bufs, x, 1);
+      if (to_root == 0) core.merge(bufs, x, 1);
     }
   };
   int stage = 0;
@@ -919,19 +922,19 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     join_warps();
     if constexpr (kUnits) {
       if (a.cluster > 1) {
-        // the CTAs' results: the first CTA's warps take those of two CTAs each, in
-        // order of rank, and join theirs
+        // the CTAs' results: the first CTA's warps take those of up to two CTAs
+        // each, in order of rank, and join theirs
         const int rank = blockIdx.x % a.cluster;
         static_assert(Core::kParts * Core::kBuf <= kWarps * kStages * Core::kStage, "ring");
         float4* all = reinterpret_cast<float4*>(rings);  // every copy has been used
-        if (warp == 0 && rank > 0)
 #pragma unroll
-          for (int x = 0; x < Core::kParts; ++x) core.put(all + x * (Core::kBuf / 16), x);
+        for (int x = 0; x < Core::kParts; ++x)
+          if (warp == root_of(x)) core.put(all + x * (Core::kBuf / 16), x);
         cluster_sync();
         if (rank == 0) {
-          if (warp > 0) core.clear();
+          core.clear();
 #pragma unroll 1
-          for (int src = warp > 0 ? warp : kWarps; src < a.cluster; src += kWarps)
+          for (int src = warp; src < a.cluster; src += kWarps)
 #pragma unroll
             for (int x = 0; x < Core::kParts; ++x)
               core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x, 0);
@@ -940,12 +943,18 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
         cluster_sync();  // no CTA ends while its buffers are read
         if (rank > 0) break;
       }
-      if (warp == 0) core.emit(a, q_row, heads, true, 0);
+#pragma unroll
+      for (int x = 0; x < Core::kParts; ++x)
+        if (warp == root_of(x)) core.emit(a, q_row, heads, true, 0, x);
       break;
     } else {
+      const int tiles = (was.len + kTile - 1) / kTile;
+#pragma unroll
+      for (int x = 0; x < Core::kParts; ++x)
+        if (warp == root_of(x))
+          core.emit(a, q_row, heads, was.steps == tiles, blockIdx.x * 2ll + (was.t0 == 0 ? 1 : 0),
+                    x);
       if (warp == 0) {
-        const int tiles = (was.len + kTile - 1) / kTile;
-        core.emit(a, q_row, heads, was.steps == tiles, blockIdx.x * 2ll + (was.t0 == 0 ? 1 : 0));
         if (lane == 0 && was.t0 == 0 && (a.by_unit || was.steps < tiles)) {
           // the group of CTAs whose range holds the unit's last tile
           const unsigned long long past = end - was.left + tiles;
