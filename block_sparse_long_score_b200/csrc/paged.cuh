@@ -28,10 +28,9 @@ inline int page_shift_of(int page_size) {
 inline int check_pool(int nseq, int page_size, int num_pages, int max_pages) {
   if (nseq < 1 || page_size < 1 || num_pages < 1 || max_pages < 1) return XATTN_ERR_INVALID_ARG;
   if (page_shift_of(page_size) < 0) return XATTN_ERR_UNSUPPORTED;
-  // slots and token positions are int32
-  constexpr long long kMost = (1ll << 31) - 1;
-  if (static_cast<long long>(num_pages) * page_size > kMost ||
-      static_cast<long long>(max_pages) * page_size > kMost || nseq > (1 << 20))
+  // slots and token positions are int32, the latter with room to count past the last
+  if (static_cast<long long>(num_pages) * page_size > (1ll << 31) - 1 ||
+      static_cast<long long>(max_pages) * page_size > 1ll << 30 || nseq > (1 << 20))
     return XATTN_ERR_UNSUPPORTED;
   return XATTN_OK;
 }

@@ -43,7 +43,7 @@ namespace {
 using host::make_pages_map;
 
 constexpr int kWarps = 4;
-constexpr int kMaxCtas = 1024;  // CTAs of the first kernel (bounds the workspace)
+constexpr int kMaxCtas = 640;  // of the split by ranges (bounds the workspace)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -67,7 +67,7 @@ struct DecodeArgs {
   // workspace: per CTA a Split and two partial results of `per` heads
   Split* split;
   float2* part_ml;  // [CTA][2][per]: maximum (base 2) and sum
-  float* part_o;    // [CTA][2][per][d], features in the warps' order
+  float* part_o;    // [CTA][2][per][d]
 };
 
 __device__ __forceinline__ int clamped(const DecodeArgs& a, int len) {

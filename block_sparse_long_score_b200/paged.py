@@ -47,6 +47,10 @@ def decode_buffers(Q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor) 
 class PagedCache:
     """Keys and values of up to ``nseq`` requests in ``num_pages`` pages.
 
+    A step that would need more pages than are free enters nothing: lengths and
+    tables stay as they are, the attention sees the tokens there were, and
+    xattn_get_device_status returns XATTN_ERR_PAGES.
+
     Attributes (device tensors, all updated in place, so a captured CUDA graph
     stays valid): ``k_pages``, ``v_pages`` [num_pages, hkv, page_size, d];
     ``table`` int32 [nseq, max_pages]; ``lens`` int32 [nseq]; ``ring``, ``pool``

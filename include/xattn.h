@@ -467,8 +467,8 @@ typedef struct {
  * gives its tokens the slot -1 and is reported as XATTN_ERR_INVALID_ARG.
  * A page belongs to one row: rows that share pages cannot both end.
  * Errors: INVALID_ARG (NULL pointer, a size below 1, max_tokens < 0),
- * UNSUPPORTED (page_size, num_pages * page_size or max_pages * page_size above
- * 2^31 - 1, nseq > 2^20), CUDA.
+ * UNSUPPORTED (page_size, num_pages * page_size above 2^31 - 1, max_pages *
+ * page_size above 2^30, nseq > 2^20; these hold for all three calls), CUDA.
  */
 int xattn_paged_plan(int nseq, int page_size, int num_pages, int max_pages, int max_tokens,
                      const int32_t* lens, const int32_t* fresh, const int32_t* pool,

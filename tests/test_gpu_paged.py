@@ -202,9 +202,10 @@ def test_plan_uses_every_free_page_and_a_full_ring_wraps():
 
 def _pool(N, hkv, page, d, dtype, order, fill=float("nan")):
     shape = {"head": (N, hkv, page, d), "token": (N, page, hkv, d), "both": (N, 2, hkv, page, d),
-             "wide": (N, hkv, page, d + 64)}[order]
+             "wide": (N, hkv, page, d + 64), "odd": (N, hkv, page, d + 8)}[order]
     def view(x):
-        return {"head": x, "token": x.transpose(1, 2), "wide": x[..., 16:16 + d]}[order]
+        return {"head": x, "token": x.transpose(1, 2), "wide": x[..., 16:16 + d],
+                "odd": x[..., 8:]}[order]
     if order == "both":
         x = torch.full(shape, fill, dtype=dtype, device=DEV)
         return x[:, 0], x[:, 1]
@@ -357,7 +358,7 @@ def test_decode_groups(group, dtype, d):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
-@pytest.mark.parametrize("order", ["head", "token", "both", "wide"])
+@pytest.mark.parametrize("order", ["head", "token", "both", "wide", "odd"])
 @pytest.mark.parametrize("dtype", [BF, F3])
 def test_decode_pages_and_strides(page, order, dtype):
     _check_decode(*_cache([page - 1, page, page + 1, 5 * page + 3, 1], 8, 2, 64, dtype, page,
@@ -429,7 +430,7 @@ def test_decode_narrow_and_wide_tables_agree():
 def test_decode_table_of_more_than_2_to_31_entries():
     """A table whose capacity is past 2^31 tiles and whose last rows lie past
     2^31 entries: only the entries of the lengths are read."""
-    n, columns = 260, (1 << 31) // 256 - 1
+    n, columns = 520, (1 << 30) // 256
     Q, kp, vp, table, lens = _cache([0] * (n - 3) + [700, 0, 300], 8, 2, 128, BF, 256)
     big = torch.empty(n, columns, dtype=torch.int32, device=DEV)
     assert big.numel() > 1 << 31

@@ -57,7 +57,7 @@ BAD_SHAPES = [
 
 @pytest.mark.parametrize("kw,code", BAD_SHAPES + [(dict(max_pages=0), -1), (dict(hq=0), -1),
                                                   (dict(hq=7), -1), (dict(hq=512), -2),
-                                                  (dict(max_pages=1 << 27), -2)])
+                                                  (dict(max_pages=(1 << 26) + 1), -2)])
 def test_decode_refuses_bad_shapes(lib, kw, code):
     s = _shape(**kw)
     assert _decode(lib, s) == code
@@ -108,7 +108,7 @@ def _plan(lib, nseq=2, page=16, pages=16, rows=8, tokens=4, **kw):
 def test_plan_refuses_bad_arguments(lib):
     for kw, code in ((dict(nseq=0), -1), (dict(page=0), -1), (dict(page=17), -2),
                      (dict(pages=0), -1), (dict(rows=0), -1), (dict(tokens=-1), -1),
-                     (dict(pages=1 << 27), -2), (dict(rows=1 << 27), -2),
+                     (dict(pages=1 << 27), -2), (dict(rows=(1 << 26) + 1), -2),
                      (dict(nseq=(1 << 20) + 1), -2)):
         assert _plan(lib, **kw) == code, kw
     for name in ("lens", "fresh", "pool", "ring", "table", "lens_out", "pool_out", "starts",
