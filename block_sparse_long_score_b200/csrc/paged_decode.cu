@@ -5,7 +5,9 @@
 //   s[h, t] = q_h . k_t / sqrt(d),  o_h = sum_t e^(s - lse_h) v_t,  lse_h = log sum_t e^s.
 // K and V are read once, which bounds the call: 2 * d * esize bytes a token
 // against 4 * g * d flops, g flops a byte in bf16 (26 TFLOP/s at the measured
-// copy rate for g = 4).
+// copy rate for g = 4). Measured, 32 query and 8 KV heads of 128 in bf16: one
+// request of 131072 tokens 87.4 us (6.1 TB/s, 94 % of the copy rate), 64 of up to
+// 8192 161 us (95 %), one of 517 8.4 us.
 //
 // Work split. A unit is a request's KV head; its tokens are cut into tiles of
 // kWarps * kChunk. Two ways, chosen on the host by what the table can hold:
