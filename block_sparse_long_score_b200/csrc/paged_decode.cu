@@ -11,19 +11,22 @@
 //
 // Work split. A unit is a request's KV head; its tokens are cut into tiles of
 // kWarps * kChunk. Two ways, chosen on the host by what the table can hold:
-//  * Ranges. The tiles of all units are numbered in a row and each CTA takes an
-//    equal range of them, whatever the lengths: one long request and many
-//    ragged ones load the GPU alike. A unit inside one CTA's range is written
+//  * Ranges. The tiles of all units are numbered in a row (and each unit counts
+//    two more, for what it costs beyond them), and each CTA takes an equal range,
+//    whatever the lengths: one long request and many ragged ones load the GPU
+//    alike. A unit inside one CTA's range is written
 //    straight to O; one that several CTAs share leaves a partial result
 //    (running maximum, sum, unnormalised o) in the workspace, at most two a
 //    CTA, and a second kernel, launched with programmatic stream
 //    serialization, joins them in CTA order.
 //  * Units. Each unit goes to a CTA, or to a cluster of CTAs whose results meet
 //    through distributed shared memory: one launch, no scan of the lengths and
-//    no workspace. For many more units than the GPU has room for, which the
-//    block scheduler balances (256 requests of up to 500 tokens, 8 KV heads:
-//    66.4 us in ranges), and for tables of so few tokens that latency is all
-//    (one request of 517 tokens: 10.5 us in ranges).
+//    no workspace. For tables of so few tokens that latency is all (one request
+//    of 517 tokens: 8.4 us, 10.5 in ranges), and for many more units than the GPU
+//    has room for, which the block scheduler balances (256 requests of up to 500
+//    tokens, 8 KV heads: 49.1 us, 54.5 in ranges; of up to 2000: 159.6 and 169);
+//    the latter only where no unit can be long, as one CTA would be left with it
+//    (60000 tokens among 255 x 200: 632 us by units, 82 in ranges).
 // Both work the bounds out on the device from lens, so a captured graph follows
 // the lengths.
 //
@@ -46,6 +49,11 @@ using host::make_pages_map;
 
 constexpr int kWarps = 4;
 constexpr int kMaxCtas = 640;  // of the split by ranges (bounds the workspace)
+// What a unit costs a CTA beyond its tiles (Q, the join of the warps, the result),
+// in tiles. Ranges of equal tiles alone end far apart where short requests lie
+// together (256 requests of up to 500 tokens in a wide table: 66 us; with a cost of
+// 1, 2, 3 tiles a unit 55.7, 54.5, 55.2; 8 of up to 2500: 18.6; 18.0, 17.4, 17.3).
+constexpr unsigned kUnitCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -641,7 +649,7 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float x, float y) {
 
 // Part of a unit that a CTA has.
 struct Unit {
-  unsigned left;  // tiles of the CTA's range from this unit's first on
+  unsigned left;  // of the CTA's range from this unit's first tile on
   int request, len, head, t0, steps;  // t0: its first tile here; steps: tiles here
 };
 
@@ -703,8 +711,12 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   Unit use;
   bool bad = false;
   [[maybe_unused]] unsigned total = 0, end = 0, groups = 0;  // of the split into ranges
-  auto next_unit = [&](Unit& u) {  // within the range: u.left > u.steps
-    u.left -= u.steps;
+  // The range goes on into another unit's tiles.
+  auto goes_on = [](const Unit& u) {
+    return u.left > static_cast<unsigned>(u.steps) + kUnitCost;
+  };
+  auto next_unit = [&](Unit& u) {
+    u.left -= u.steps + kUnitCost;
     u.t0 = 0;
     if (++u.head == D.hkv) {
       u.head = 0;
@@ -736,6 +748,9 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     asm volatile("griddepcontrol.launch_dependents;");
     // Where the range begins: a scan of the requests' tile counts, a run of
     // requests to each thread. (The host has made sure of fewer than 2^31 tiles.)
+    auto cost_of = [](int len) {  // in tiles; the unit's own cost comes first
+      return len == 0 ? 0 : (len + kTile - 1) / kTile + kUnitCost;
+    };
     const int launched = gridDim.x / a.hc;
     const int run = (D.nseq + kThreads - 1) / kThreads;
     const int i0 = min(tid * run, D.nseq), i1 = min(i0 + run, D.nseq);
@@ -747,7 +762,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       len = clamped(a, raw);
       bad = bad || len != raw;
       empty = empty || len == 0;
-      mine += (len + kTile - 1) / kTile;
+      mine += cost_of(len);
     }
     if (bad && blockIdx.x == 0) atomicExch(a.status, kStatusBadCache);
     bad = false;
@@ -782,7 +797,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     if (pos >= before && pos < upto * D.hkv) {
       for (int i = i0; i < i1; ++i) {
         if (run > 1) len = clamped(a, a.lens[i]);
-        const unsigned next = before + static_cast<unsigned>((len + kTile - 1) / kTile) * D.hkv;
+        const unsigned next = before + cost_of(len) * D.hkv;
         if (pos < next) {
           s_request = i;
           s_len = len;
@@ -793,13 +808,16 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       }
     }
     __syncthreads();
-    use.left = end - pos;
     use.request = s_request;
     use.len = s_len;
-    const unsigned tiles = (use.len + kTile - 1) / kTile;
-    use.head = static_cast<int>((pos - s_before) / tiles);
-    use.t0 = static_cast<int>((pos - s_before) % tiles);
-    use.steps = static_cast<int>(min(tiles - use.t0, use.left));
+    const unsigned cost = cost_of(use.len), at = (pos - s_before) % cost;
+    use.head = static_cast<int>((pos - s_before) / cost);
+    use.t0 = static_cast<int>(max(at, kUnitCost) - kUnitCost);
+    use.left = end - pos;
+    const unsigned skip = max(at, kUnitCost) - at;
+    if (use.left <= skip) return;  // it ends before the unit's first tile
+    use.left -= skip;
+    use.steps = static_cast<int>(min(cost - kUnitCost - use.t0, use.left));
   }
   // Two of these walk the range's units: one issues copies, the other, some
   // stages behind, uses them.
@@ -850,7 +868,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
         }
       }
       if (++step == ahead.steps) {
-        done = ahead.left == static_cast<unsigned>(ahead.steps);
+        done = !goes_on(ahead);
         if (!done) {
           next_unit(ahead);
           step = 0;
@@ -915,7 +933,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
 
     const Unit was = use;
     const long long q_row = q_row_of(was);
-    const bool last = was.left == static_cast<unsigned>(was.steps);
+    const bool last = !goes_on(was);
     if (!last) {  // the next unit's Q, while this one's results are joined
       next_unit(use);
       core.fetch(a, q_row_of(use), heads);
@@ -1103,12 +1121,14 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
 
-  // By units: four waves of them balance themselves; fewer where the table holds
-  // so little that a unit's CTA, or each of its cluster, has eight tiles at most.
+  // By units: four waves of them, of 32 tiles at most, balance themselves; fewer
+  // where the table holds so little that a unit's CTA, or each of its cluster, has
+  // eight tiles at most; and where the tiles of all cannot be numbered.
   a.cluster = 1;
   while (a.cluster < 8 && a.cluster < row_tiles && 2 * a.cluster * units <= slots) a.cluster *= 2;
-  if (units >= 4 * slots || row_tiles <= 8 * a.cluster || tiles >= 1ll << 31) {
-    if (units >= 4 * slots || tiles >= 1ll << 31) a.cluster = 1;
+  const bool waves = units >= 4 * slots && row_tiles <= 32;
+  const bool numbered = tiles + kUnitCost * D.nseq * static_cast<long long>(D.hkv) < 1ll << 31;
+  if (waves || row_tiles <= 8 * a.cluster || !numbered) {
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, true>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          smem_of<Core>());
