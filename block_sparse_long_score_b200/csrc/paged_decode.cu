@@ -10,7 +10,7 @@
 // 8192 161 us (95 %), one of 517 8.4 us.
 //
 // Work split. A unit is a request's KV head; its tokens are cut into tiles of
-// kWarps * kChunk. Two ways, chosen on the host by what the table can hold:
+// kWarps * kChunk. Three ways, chosen on the host by what the table can hold:
 //  * Ranges. The tiles of all units are numbered in a row (and each unit counts
 //    two more, for what it costs beyond them), and each CTA takes an equal range,
 //    whatever the lengths: one long request and many ragged ones load the GPU
@@ -27,10 +27,17 @@
 //    tokens, 8 KV heads: 49.1 us, 54.5 in ranges; of up to 2000: 159.6 and 169);
 //    the latter only where no unit can be long, as one CTA would be left with it
 //    (60000 tokens among 255 x 200: 632 us by units, 82 in ranges).
-// Both work the bounds out on the device from lens, so a captured graph follows
+//  * Warps. Each unit goes to one warp, whose tiles are single chunks: the warps
+//    share nothing, and the four units of a CTA overlap. For many units of few
+//    tokens, which a CTA would start, join and end for too little (1024 requests of
+//    up to 100 tokens: 45.2 us, 84.1 with a CTA a unit; 512 of up to 250: 49.3 and
+//    57.2; 512 of up to 250 in fp32: 92 and 111; but 256 of up to 1000: 92 and 86,
+//    512 of up to 1000, d = 64: 95 and 87, as the warps that are left at the end
+//    load little). Not where a CTA's warps share Q.
+// All work the bounds out on the device from lens, so a captured graph follows
 // the lengths.
 //
-// Inside a CTA the warps take the tile's chunks, each with its own running
+// Inside a CTA with a unit the warps take the tile's chunks, each with its own running
 // maximum, sum and o; they meet once at the end of a unit. A warp's K and V come
 // by TMA through a ring of stages in shared memory of its own, so a stage
 // passes between a warp's lanes only: no CTA-wide barrier in the loop, and the
@@ -660,13 +667,14 @@ __device__ __forceinline__ const float4* in_cluster(const float4* p, int rank) {
   return reinterpret_cast<const float4*>(r);
 }
 
-// O = 0 and lse = -inf for the requests that hold nothing.
+// O = 0 and lse = -inf for a request that holds nothing, by `threads` threads of
+// which this is number t; and for all such requests.
 template <class Core>
 __device__ __forceinline__ void empty_row(const DecodeArgs& a, int request, int head, int head0,
-                                          int heads) {
+                                          int heads, int t, int threads) {
   constexpr int kHalf = Core::kDim / 2;
   const long long row = static_cast<long long>(request) * a.D.hq + head * a.D.group + head0;
-  for (int x = threadIdx.x; x < heads * kHalf; x += kWarps * 32) {
+  for (int x = t; x < heads * kHalf; x += threads) {
     store_pair(static_cast<typename Core::T*>(a.O) + row * Core::kDim + 2 * x, 0.0f, 0.0f);
     if (x % kHalf == 0 && a.lse != nullptr) a.lse[row + x / kHalf] = -INFINITY;
   }
@@ -677,25 +685,32 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
   for (int i = group; i < a.D.nseq; i += groups) {
     if (clamped(a, a.lens[i]) != 0) continue;
     for (int head = 0; head < a.D.hkv; ++head) {
-      empty_row<Core>(a, i, head, head0, heads);
+      empty_row<Core>(a, i, head, head0, heads, threadIdx.x, kWarps * 32);
       if (a.by_unit && threadIdx.x == 0) split_of(a, i, head, part)->more = 0;
     }
   }
 }
 
-template <class Core, bool kUnits>
+// How the work is cut (see above).
+enum Way { kByRanges, kByUnits, kByWarps };
+
+template <class Core, Way kWay>
 __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using T = typename Core::T;
-  constexpr int kTile = kWarps * Core::kChunk, kThreads = kWarps * 32;
+  constexpr bool kUnits = kWay != kByRanges, kAlone = kWay == kByWarps;
+  constexpr int kTile = (kAlone ? 1 : kWarps) * Core::kChunk, kThreads = kWarps * 32;
   constexpr int kStages = stages_of<Core>();
+  static_assert(!kAlone || !Core::kQShared, "a warp's Q is in its registers");
   const PagedDims& D = a.D;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   // CTAs (clusters) b * hc .. b * hc + hc - 1 take the same tiles for different
   // heads of the group, at about the same time: the second to read a row finds
   // it in L2.
-  const int block = kUnits ? blockIdx.x / a.cluster : blockIdx.x;
+  const int block = kAlone   ? blockIdx.x * kWarps + warp
+                    : kUnits ? blockIdx.x / a.cluster
+                             : blockIdx.x;
   const int part = block % a.hc, group = block / a.hc;
   const int head0 = part * a.per, heads = min(a.per, D.group - head0);
 
@@ -726,14 +741,18 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     u.steps = static_cast<int>(min(static_cast<unsigned>((u.len + kTile - 1) / kTile), u.left));
   };
   if constexpr (kUnits) {
-    const int rank = blockIdx.x % a.cluster;
+    __syncthreads();  // s_abort
+    const int rank = kAlone ? 0 : blockIdx.x % a.cluster;
+    if (kAlone && group >= D.nseq * D.hkv) return;
     use.request = group / D.hkv;
     use.head = group % D.hkv;
     const int raw = a.lens[use.request];
     use.len = clamped(a, raw);
-    if (use.len != raw && rank == 0 && tid == 0) atomicExch(a.status, kStatusBadCache);
+    if (use.len != raw && rank == 0 && lane == 0) atomicExch(a.status, kStatusBadCache);
     if (use.len == 0) {  // so for the whole cluster
-      if (rank == 0) empty_row<Core>(a, use.request, use.head, head0, heads);
+      if (rank == 0)
+        empty_row<Core>(a, use.request, use.head, head0, heads, kAlone ? lane : tid,
+                        kAlone ? 32 : kThreads);
       return;
     }
     const unsigned tiles = (use.len + kTile - 1) / kTile;
@@ -741,7 +760,6 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     use.steps =
         static_cast<int>(static_cast<unsigned long long>(tiles) * (rank + 1) / a.cluster) - use.t0;
     use.left = use.steps;
-    __syncthreads();
   } else {
     __shared__ unsigned s_sum[kWarps], s_before;
     __shared__ int s_request, s_len;
@@ -836,9 +854,10 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   core.fetch(a, q_row_of(use), heads);
 
   // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
+  const int in_tile = kAlone ? 0 : warp * Core::kChunk;  // the warp's place in a tile
   int step = 0, pages = -1, pages_next = -1;
   auto page_batch = [&](const Unit& u, int step0) {
-    const int t = (u.t0 + step0 + lane) * kTile + warp * Core::kChunk;
+    const int t = (u.t0 + step0 + lane) * kTile + in_tile;
     if (step0 + lane >= u.steps || t >= u.len) return -1;
     const int page = a.table[static_cast<long long>(u.request) * D.max_pages +
                              (t >> D.page_shift)];
@@ -855,7 +874,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     int valid = 0;
     if (!done) {
       const int page = __shfl_sync(0xffffffffu, pages, step % 32);
-      const int t = (ahead.t0 + step) * kTile + warp * Core::kChunk;
+      const int t = (ahead.t0 + step) * kTile + in_tile;
       if (page >= 0) {
         valid = min(Core::kChunk, ahead.len - t);
         __syncwarp();  // every lane is done with the stage
@@ -939,6 +958,11 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       core.fetch(a, q_row_of(use), heads);
     }
 
+    if constexpr (kAlone) {
+#pragma unroll
+      for (int x = 0; x < Core::kParts; ++x) core.emit(a, q_row, heads, true, 0, x);
+      break;
+    }
     join_warps();
     if constexpr (kUnits) {
       if (a.cluster > 1) {
@@ -1121,6 +1145,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
 
+  // By warps: two waves of units or more, of 32 steps of a warp at most.
   // By units: four waves of them, of 32 tiles at most, balance themselves; fewer
   // where the table holds so little that a unit's CTA, or each of its cluster, has
   // eight tiles at most; and where the tiles of all cannot be numbered.
@@ -1128,8 +1153,19 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   while (a.cluster < 8 && a.cluster < row_tiles && 2 * a.cluster * units <= slots) a.cluster *= 2;
   const bool waves = units >= 4 * slots && row_tiles <= 32;
   const bool numbered = tiles + kUnitCost * D.nseq * static_cast<long long>(D.hkv) < 1ll << 31;
+  if constexpr (!Core::kQShared) {
+    if (units >= 2 * slots && row_tiles <= 8) {
+      cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByWarps>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           smem_of<Core>());
+      if (e != cudaSuccess) return e;
+      const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
+      decode_kernel<Core, kByWarps><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
+      return cudaGetLastError();
+    }
+  }
   if (waves || row_tiles <= 8 * a.cluster || !numbered) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, true>,
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByUnits>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          smem_of<Core>());
     if (e != cudaSuccess) return e;
@@ -1139,17 +1175,17 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
     cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
     cfg.dynamicSmemBytes = smem_of<Core>();
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<Core, true>, a, k_map, v_map);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<Core, kByUnits>, a, k_map, v_map);
   }
 
   // By ranges, no more than there can be tiles.
   const unsigned grid = static_cast<unsigned>(max(1ll, min(slots / a.hc, tiles)) * a.hc);
   a.by_unit = units < grid;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, false>,
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByRanges>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem_of<Core>());
   if (e != cudaSuccess) return e;
-  decode_kernel<Core, false><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
+  decode_kernel<Core, kByRanges><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -387,6 +387,42 @@ def test_decode_many_requests(n, dtype):
     _check_decode(*_cache([rng.choice((0, 1, 5, 17, 40)) for _ in range(n)], 2, 1, 64, dtype, 16))
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F3, 128), (F3, 64), (F3, 32)])
+@pytest.mark.parametrize("group", [1, 3, 8, 13])
+def test_decode_many_short_requests(group, dtype, d):
+    """More units (an odd number of them) than the GPU has room for twice, none longer
+    than a row of the table of 256 (fp32) or 512 tokens: a warp takes each."""
+    rng = random.Random(group * d)
+    longest = 480 if dtype is BF else 230
+    lens = [rng.choice((0, 1, 7, 8, 9, 15, 16, 17, 63, 65, 128, 200, longest - 1, longest))
+            for _ in range(187)]
+    lens[3] = longest
+    _check_decode(*_cache(lens, 7 * group, 7, d, dtype, 16, seed=group))
+
+
+@pytest.mark.parametrize("dtype", [BF, F3])
+def test_decode_many_short_requests_with_bad_pages_and_lengths(dtype):
+    Q, kp, vp, table, lens = _cache([20, 100, 33] * 63, 21, 7, 64, dtype, 16)
+    table = table[:, :7].contiguous()
+    table[5, 1] = -1
+    table[7, 6] = 1 << 30
+    table[9, 0] = kp.shape[0]
+    _check_decode(Q, kp, vp, table, lens, status=-1)
+    kp.nan_to_num_(), vp.nan_to_num_()       # the whole row of request 188 is read
+    lens[10] = -1
+    lens[188] = 1 << 30
+    table[188] = table[1]
+    _check_decode(Q, kp, vp, table, lens, status=-1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F3])
+def test_decode_one_long_request_among_many_short_ones(dtype):
+    """Far more tokens in one request than in all the others."""
+    lens = [(37 * i) % 70 for i in range(220)]
+    lens[100] = 20011
+    _check_decode(*_cache(lens, 16, 8, 64, dtype, 64))
+
+
 def _wide(Q, kp, vp, table, lens, columns):
     """The same requests in a table with room for far more tokens: the work is
     cut by tile ranges, where a narrow table's goes to CTAs or clusters by unit."""
