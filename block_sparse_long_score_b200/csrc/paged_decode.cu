@@ -33,7 +33,12 @@
 //    up to 100 tokens: 45.2 us, 84.1 with a CTA a unit; 512 of up to 250: 49.3 and
 //    57.2; 512 of up to 250 in fp32: 92 and 111; but 256 of up to 1000: 92 and 86,
 //    512 of up to 1000, d = 64: 95 and 87, as the warps that are left at the end
-//    load little). Not where a CTA's warps share Q.
+//    load little). Not where a CTA's warps share Q. Where the table could hold long
+//    requests and there are as many units, the split by ranges looks at the lengths
+//    and gives each warp the units that begin in its own equal range (1024 of up to
+//    100: 57 us, 86 by CTAs' ranges; 512 of up to 130: 42 and 50; 512 of up to 60 in
+//    fp32: 41 and 73; at the bound 800 of up to 250: 91 and 88, 512 of up to 250 with
+//    d = 64: 35 and 39).
 // All work the bounds out on the device from lens, so a captured graph follows
 // the lengths.
 //
@@ -44,6 +49,8 @@
 // copies run ahead across unit boundaries.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "host.cuh"
 #include "paged.cuh"
@@ -60,7 +67,10 @@ constexpr int kMaxCtas = 640;  // of the split by ranges (bounds the workspace)
 // in tiles. Ranges of equal tiles alone end far apart where short requests lie
 // together (256 requests of up to 500 tokens in a wide table: 66 us; with a cost of
 // 1, 2, 3 tiles a unit 55.7, 54.5, 55.2; 8 of up to 2500: 18.6; 18.0, 17.4, 17.3).
-constexpr unsigned kUnitCost = 2;
+constexpr int kUnitCost = 2;
+// By warps: no unit of more tiles than this (half of it where the warps' ranges are
+// fixed beforehand, whose ends lie up to a unit apart), and this many units a CTA.
+constexpr int kAloneTiles = 8, kAloneWaves = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -160,6 +170,7 @@ struct CoreBf16 {
   // Q: in registers for up to 8 heads. For more it would take half of them, and
   // sits in shared memory, swizzled like K.
   static constexpr bool kQShared = NT > 1;
+  static constexpr bool kAloneInRanges = !kQShared;  // see decode_kernel
   static constexpr int kQBytes = kQShared ? 8 * NT * kD * 2 : 0;
   static constexpr int kQEach = kQShared ? kQBytes / 16 / (kWarps * 32) : 1;
   uint4 fetched[kQEach];
@@ -407,6 +418,9 @@ struct CoreF32 {
   static constexpr bool kSpread = false;       // (all heads' maxima come with the first)
   static constexpr int kBuf = (kPart * kPieces + 1) * 512;
   static constexpr bool kQShared = false;
+  // (of 8 heads the kernel with both walks takes 74.8 us where the one by CTAs takes
+  // 69.8: 16 requests of up to 16384 tokens, d = 64)
+  static constexpr bool kAloneInRanges = H < 8;
   static constexpr int kQBytes = 0;
   using T = float;
   using F2 = unsigned long long;               // two floats
@@ -656,7 +670,7 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float x, float y) {
 
 // Part of a unit that a CTA has.
 struct Unit {
-  unsigned left;  // of the CTA's range from this unit's first tile on
+  int left;  // of the range from this unit's first tile on
   int request, len, head, t0, steps;  // t0: its first tile here; steps: tiles here
 };
 
@@ -691,26 +705,30 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
   }
 }
 
-// How the work is cut (see above).
-enum Way { kByRanges, kByUnits, kByWarps };
+// How the work is cut (see above). kByRangesOrWarps chooses on the device; it is a
+// kernel of its own since its size costs short calls 0.6 us (5 requests of up to 4001
+// tokens in fp32: 12.2 us, 11.5 without the walk by warps).
+enum Way { kByRanges, kByRangesOrWarps, kByUnits, kByWarps };
 
 template <class Core, Way kWay>
 __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using T = typename Core::T;
-  constexpr bool kUnits = kWay != kByRanges, kAlone = kWay == kByWarps;
-  constexpr int kTile = (kAlone ? 1 : kWarps) * Core::kChunk, kThreads = kWarps * 32;
+  constexpr bool kUnits = kWay == kByUnits || kWay == kByWarps;
+  constexpr int kTile = kWarps * Core::kChunk, kThreads = kWarps * 32;
   constexpr int kStages = stages_of<Core>();
-  static_assert(!kAlone || !Core::kQShared, "a warp's Q is in its registers");
+  constexpr bool kMaybeAlone = kWay == kByRangesOrWarps;
+  static_assert(kWay == kByRanges || kWay == kByUnits || !Core::kQShared,
+                "a warp's Q is in its registers");
   const PagedDims& D = a.D;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   // CTAs (clusters) b * hc .. b * hc + hc - 1 take the same tiles for different
   // heads of the group, at about the same time: the second to read a row finds
   // it in L2.
-  const int block = kAlone   ? blockIdx.x * kWarps + warp
-                    : kUnits ? blockIdx.x / a.cluster
-                             : blockIdx.x;
+  const int block = kWay == kByWarps   ? blockIdx.x * kWarps + warp
+                    : kWay == kByUnits ? blockIdx.x / a.cluster
+                                       : blockIdx.x;
   const int part = block % a.hc, group = block / a.hc;
   const int head0 = part * a.per, heads = min(a.per, D.group - head0);
 
@@ -726,24 +744,26 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   Unit use;
   bool bad = false;
   [[maybe_unused]] unsigned total = 0, end = 0, groups = 0;  // of the split into ranges
-  // The range goes on into another unit's tiles.
-  auto goes_on = [](const Unit& u) {
-    return u.left > static_cast<unsigned>(u.steps) + kUnitCost;
+  bool alone = kWay == kByWarps;  // a unit is a warp's, all of it
+  auto tiles_of = [](int len) { return (len + kTile - 1) / kTile; };
+  // The range goes on into another unit's tiles, or, alone, to another unit's start.
+  auto goes_on = [&](auto alone_c, const Unit& u) {
+    return alone_c() ? u.left > tiles_of(u.len) : u.left > u.steps + kUnitCost;
   };
-  auto next_unit = [&](Unit& u) {
-    u.left -= u.steps + kUnitCost;
+  auto next_unit = [&](auto alone_c, Unit& u) {
+    u.left -= (alone_c() ? tiles_of(u.len) : u.steps) + kUnitCost;
     u.t0 = 0;
     if (++u.head == D.hkv) {
       u.head = 0;
       do u.len = clamped(a, a.lens[++u.request]);
       while (u.len == 0);
     }
-    u.steps = static_cast<int>(min(static_cast<unsigned>((u.len + kTile - 1) / kTile), u.left));
+    u.steps = alone_c() ? (u.len + Core::kChunk - 1) / Core::kChunk : min(tiles_of(u.len), u.left);
   };
   if constexpr (kUnits) {
     __syncthreads();  // s_abort
-    const int rank = kAlone ? 0 : blockIdx.x % a.cluster;
-    if (kAlone && group >= D.nseq * D.hkv) return;
+    const int rank = alone ? 0 : blockIdx.x % a.cluster;
+    if (alone && group >= D.nseq * D.hkv) return;
     use.request = group / D.hkv;
     use.head = group % D.hkv;
     const int raw = a.lens[use.request];
@@ -751,37 +771,40 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     if (use.len != raw && rank == 0 && lane == 0) atomicExch(a.status, kStatusBadCache);
     if (use.len == 0) {  // so for the whole cluster
       if (rank == 0)
-        empty_row<Core>(a, use.request, use.head, head0, heads, kAlone ? lane : tid,
-                        kAlone ? 32 : kThreads);
+        empty_row<Core>(a, use.request, use.head, head0, heads, alone ? lane : tid,
+                        alone ? 32 : kThreads);
       return;
     }
-    const unsigned tiles = (use.len + kTile - 1) / kTile;
+    const unsigned tiles =
+        alone ? (use.len + Core::kChunk - 1) / Core::kChunk : tiles_of(use.len);
     use.t0 = static_cast<int>(static_cast<unsigned long long>(tiles) * rank / a.cluster);
     use.steps =
         static_cast<int>(static_cast<unsigned long long>(tiles) * (rank + 1) / a.cluster) - use.t0;
-    use.left = use.steps;
+    use.left = 0;
   } else {
-    __shared__ unsigned s_sum[kWarps], s_before;
-    __shared__ int s_request, s_len;
+    __shared__ unsigned s_sum[kWarps], s_before[kWarps];
+    __shared__ int s_request[kWarps], s_len[kWarps], s_longest[kWarps], s_held[kWarps];
     asm volatile("griddepcontrol.launch_dependents;");
     // Where the range begins: a scan of the requests' tile counts, a run of
     // requests to each thread. (The host has made sure of fewer than 2^31 tiles.)
-    auto cost_of = [](int len) {  // in tiles; the unit's own cost comes first
-      return len == 0 ? 0 : (len + kTile - 1) / kTile + kUnitCost;
+    auto cost_of = [&](int len) {  // in tiles; the unit's own cost comes first
+      return len == 0 ? 0 : tiles_of(len) + kUnitCost;
     };
     const int launched = gridDim.x / a.hc;
     const int run = (D.nseq + kThreads - 1) / kThreads;
     const int i0 = min(tid * run, D.nseq), i1 = min(i0 + run, D.nseq);
     unsigned mine = 0;
     int len = 0;
-    bool empty = false;
+    int longest = 0, held = 0;  // of these requests; those that hold tokens
     for (int i = i0; i < i1; ++i) {
       const int raw = a.lens[i];
       len = clamped(a, raw);
       bad = bad || len != raw;
-      empty = empty || len == 0;
+      longest = max(longest, len);
+      held += len > 0;
       mine += cost_of(len);
     }
+    const bool none = held < i1 - i0;
     if (bad && blockIdx.x == 0) atomicExch(a.status, kStatusBadCache);
     bad = false;
     unsigned upto = mine;
@@ -791,227 +814,269 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       if (lane >= x) upto += y;
     }
     if (lane == 31) s_sum[warp] = upto;
-    empty = __syncthreads_or(empty);
+    if (kMaybeAlone) {
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      held = __reduce_add_sync(0xffffffffu, held);
+      if (lane == 0) s_longest[warp] = longest, s_held[warp] = held;
+    }
+    const bool empty = __syncthreads_or(none);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) upto += s_sum[w];
       total += s_sum[w];
     }
     total *= D.hkv;
+    if (kMaybeAlone) {
+      longest = held = 0;
+      for (int w = 0; w < kWarps; ++w) longest = max(longest, s_longest[w]), held += s_held[w];
+      alone = longest <= kAloneTiles / 2 * kTile && held * D.hkv >= kAloneWaves * launched;
+    }
     if (empty) empty_rows<Core>(a, group, launched, part, head0, heads);
     if (!a.by_unit && tid == 0) a.split[blockIdx.x].more = 0;
     // as many ranges as there are tiles, at most: none is empty, so a unit's
     // partial results are those of consecutive CTAs; and where there are few
     // tiles, four to a CTA rather than fewer to more of them, with more results
-    // to join (one request of 8192 tokens: 18.5 us with 444 CTAs, 15.5 with 256)
-    groups = min(static_cast<unsigned>(launched),
-                 max(total / 4, min(total, static_cast<unsigned>(a.sms))));
-    if (group >= static_cast<int>(groups)) return;
+    // to join (one request of 8192 tokens: 18.5 us with 444 CTAs, 15.5 with 256);
+    // alone, one to a warp, some of which may hold no unit's start
+    groups = alone ? launched * kWarps
+                   : min(static_cast<unsigned>(launched),
+                         max(total / 4, min(total, static_cast<unsigned>(a.sms))));
+    if (!alone && group >= static_cast<int>(groups)) return;
     // range b begins at total * b / groups
     const unsigned each = total / groups, over = total % groups;
-    const unsigned pos = group * each + group * over / groups;
-    end = (group + 1) * each + (group + 1) * over / groups;
-    unsigned before = (upto - mine) * D.hkv;
-    if (pos >= before && pos < upto * D.hkv) {
+    auto begin = [&](unsigned b) { return b * each + b * over / groups; };
+    const unsigned mine0 = (upto - mine) * D.hkv, mine1 = upto * D.hkv;
+    for (int w = 0; w < (alone ? kWarps : 1); ++w) {
+      const unsigned pos = begin(alone ? group * kWarps + w : group);
+      if (pos < mine0 || pos >= mine1) continue;
+      unsigned before = mine0;
       for (int i = i0; i < i1; ++i) {
         if (run > 1) len = clamped(a, a.lens[i]);
         const unsigned next = before + cost_of(len) * D.hkv;
         if (pos < next) {
-          s_request = i;
-          s_len = len;
-          s_before = before;
+          s_request[w] = i;
+          s_len[w] = len;
+          s_before[w] = before;
           break;
         }
         before = next;
       }
     }
     __syncthreads();
-    use.request = s_request;
-    use.len = s_len;
-    const unsigned cost = cost_of(use.len), at = (pos - s_before) % cost;
-    use.head = static_cast<int>((pos - s_before) / cost);
-    use.t0 = static_cast<int>(max(at, kUnitCost) - kUnitCost);
+    const int w = alone ? warp : 0, range = alone ? group * kWarps + warp : group;
+    const unsigned pos = begin(range);
+    end = begin(range + 1);
+    use.request = s_request[w];
+    use.len = s_len[w];
+    const unsigned cost = cost_of(use.len), at = (pos - s_before[w]) % cost;
+    use.head = static_cast<int>((pos - s_before[w]) / cost);
     use.left = end - pos;
-    const unsigned skip = max(at, kUnitCost) - at;
-    if (use.left <= skip) return;  // it ends before the unit's first tile
-    use.left -= skip;
-    use.steps = static_cast<int>(min(cost - kUnitCost - use.t0, use.left));
+    if (alone) {  // from the first unit that begins in the range
+      use.t0 = 0;
+      use.left += static_cast<int>(at) - static_cast<int>(kUnitCost);
+      use.steps = (use.len + Core::kChunk - 1) / Core::kChunk;
+      if (pos == end) return;
+      if (at > 0) {
+        if (!goes_on(std::true_type(), use)) return;
+        next_unit(std::true_type(), use);
+      }
+    } else {
+      use.t0 = static_cast<int>(max(at, static_cast<unsigned>(kUnitCost)) - kUnitCost);
+      const int skip = max(at, static_cast<unsigned>(kUnitCost)) - at;
+      if (use.left <= skip) return;  // it ends before the unit's first tile
+      use.left -= skip;
+      use.steps = min(static_cast<int>(cost - kUnitCost) - use.t0, use.left);
+    }
   }
-  // Two of these walk the range's units: one issues copies, the other, some
-  // stages behind, uses them.
-  Unit ahead = use;
+  // The units from `use` on: the CTA's warps take each together, or, alone, a warp
+  // the units that begin in its range.
+  auto walk = [&](auto alone_c) {
+    constexpr bool kAlone = decltype(alone_c)::value;
+    // Two of these walk the range's units: one issues copies, the other, some
+    // stages behind, uses them.
+    Unit ahead = use;
 
-  Core core;
-  core.init();
-  char* rings = s_dynamic + (1024 - smem_u32(s_dynamic) % 1024) % 1024;
-  char* ring = rings + warp * kStages * Core::kStage;
-  float4* bufs = reinterpret_cast<float4*>(rings + kWarps * kStages * Core::kStage);
+    Core core;
+    core.init();
+    char* rings = s_dynamic + (1024 - smem_u32(s_dynamic) % 1024) % 1024;
+    char* ring = rings + warp * kStages * Core::kStage;
+    float4* bufs = reinterpret_cast<float4*>(rings + kWarps * kStages * Core::kStage);
 
-  // Q before the copies, whose bytes it would queue behind
-  auto q_row_of = [&](const Unit& u) {
-    return static_cast<long long>(u.request) * D.hq + u.head * D.group + head0;
-  };
-  core.fetch(a, q_row_of(use), heads);
+    // Q before the copies, whose bytes it would queue behind
+    auto q_row_of = [&](const Unit& u) {
+      return static_cast<long long>(u.request) * D.hq + u.head * D.group + head0;
+    };
+    core.fetch(a, q_row_of(use), heads);
 
-  // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
-  const int in_tile = kAlone ? 0 : warp * Core::kChunk;  // the warp's place in a tile
-  int step = 0, pages = -1, pages_next = -1;
-  auto page_batch = [&](const Unit& u, int step0) {
-    const int t = (u.t0 + step0 + lane) * kTile + in_tile;
-    if (step0 + lane >= u.steps || t >= u.len) return -1;
-    const int page = a.table[static_cast<long long>(u.request) * D.max_pages +
-                             (t >> D.page_shift)];
-    if (page >= 0 && page < D.num_pages) return page;
-    bad = true;
-    return -1;
-  };
-  pages = page_batch(ahead, 0);
-  pages_next = page_batch(ahead, 32);
-  uint32_t valids = 0;  // rows of the chunks under way, 5 bits each, the newest lowest
-  bool done = use.steps == 0;  // (a CTA of a cluster may have none)
-  // Copies the warp's next chunk to a stage.
-  auto issue = [&](int stage) {
-    int valid = 0;
-    if (!done) {
-      const int page = __shfl_sync(0xffffffffu, pages, step % 32);
-      const int t = (ahead.t0 + step) * kTile + in_tile;
-      if (page >= 0) {
-        valid = min(Core::kChunk, ahead.len - t);
-        __syncwarp();  // every lane is done with the stage
-        if (elect_one()) {
-          uint64_t* full = &s_full[warp][stage];
-          char* to = ring + stage * Core::kStage;
-          mbar_arrive_expect_tx(full, Core::kStage);
-          tma_load_5d(to, &k_map, full, t & (D.page - 1), ahead.head, page);
-          tma_load_5d(to + Core::kStage / 2, &v_map, full, t & (D.page - 1), ahead.head, page);
+    // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
+    const int per_step = kAlone ? Core::kChunk : kTile;
+    const int in_step = kAlone ? 0 : warp * Core::kChunk;  // the warp's place in a step
+    int step = 0, pages = -1, pages_next = -1;
+    auto page_batch = [&](const Unit& u, int step0) {
+      const int t = (u.t0 + step0 + lane) * per_step + in_step;
+      if (step0 + lane >= u.steps || t >= u.len) return -1;
+      const int page = a.table[static_cast<long long>(u.request) * D.max_pages +
+                               (t >> D.page_shift)];
+      if (page >= 0 && page < D.num_pages) return page;
+      bad = true;
+      return -1;
+    };
+    pages = page_batch(ahead, 0);
+    pages_next = page_batch(ahead, 32);
+    uint32_t valids = 0;  // rows of the chunks under way, 5 bits each, the newest lowest
+    bool done = use.steps == 0;  // (a CTA of a cluster may have none)
+    // Copies the warp's next chunk to a stage.
+    auto issue = [&](int stage) {
+      int valid = 0;
+      if (!done) {
+        const int page = __shfl_sync(0xffffffffu, pages, step % 32);
+        const int t = (ahead.t0 + step) * per_step + in_step;
+        if (page >= 0) {
+          valid = min(Core::kChunk, ahead.len - t);
+          __syncwarp();  // every lane is done with the stage
+          if (elect_one()) {
+            uint64_t* full = &s_full[warp][stage];
+            char* to = ring + stage * Core::kStage;
+            mbar_arrive_expect_tx(full, Core::kStage);
+            tma_load_5d(to, &k_map, full, t & (D.page - 1), ahead.head, page);
+            tma_load_5d(to + Core::kStage / 2, &v_map, full, t & (D.page - 1), ahead.head, page);
+          }
+        }
+        if (++step == ahead.steps) {
+          done = kUnits || !goes_on(alone_c, ahead);
+          if (!done) {
+            next_unit(alone_c, ahead);
+            step = 0;
+            pages = page_batch(ahead, 0);
+            pages_next = page_batch(ahead, 32);
+          }
+        } else if (step % 32 == 0) {
+          pages = pages_next;
+          pages_next = page_batch(ahead, step + 32);
         }
       }
-      if (++step == ahead.steps) {
-        done = !goes_on(ahead);
-        if (!done) {
-          next_unit(ahead);
-          step = 0;
-          pages = page_batch(ahead, 0);
-          pages_next = page_batch(ahead, 32);
-        }
-      } else if (step % 32 == 0) {
-        pages = pages_next;
-        pages_next = page_batch(ahead, step + 32);
-      }
-    }
-    valids = valids << 5 | static_cast<unsigned>(valid);
-  };
-  for (int x = 0; x < kStages; ++x) issue(x);
+      valids = valids << 5 | static_cast<unsigned>(valid);
+    };
+    for (int x = 0; x < kStages; ++x) issue(x);
 
-  // The warps' results of a unit, joined in a fixed order. Part x ends up in warp
-  // root_of(x), so that several warps can write a unit's heads out: it takes warp
-  // root ^ 2's, warp root ^ 1 takes root ^ 3's, and then root root ^ 1's.
-  // (bufs[0] is read last, and is not the one that takes the next unit's Q)
-  auto root_of = [](int x) { return Core::kSpread ? x % kWarps : 0; };
-  auto join_warps = [&]() {
+    // The warps' results of a unit, joined in a fixed order. Part x ends up in warp
+    // root_of(x), so that several warps can write a unit's heads out: it takes warp
+    // root ^ 2's, warp root ^ 1 takes root ^ 3's, and then root root ^ 1's.
+    // (bufs[0] is read last, and is not the one that takes the next unit's Q)
+    auto root_of = [](int x) { return Core::kSpread ? x % kWarps : 0; };
+    auto join_warps = [&]() {
 #pragma unroll
-    for (int x = 0; x < Core::kParts; ++x) {
-      const int to_root = warp ^ root_of(x);
-      float4* buf = bufs + (1 - to_root % 2) * (Core::kBuf / 16);
-      __syncthreads();
-      if (to_root >= 2) core.put(buf, x);
-      __syncthreads();
-      if (to_root < 2) core.merge(buf, x, 0);
-      if (to_root == 1) core.put(buf, x);
-      __syncthreads();
-      if (to_root == 0) core.merge(bufs, x, 1);
-    }
-  };
-  int stage = 0;
-  uint32_t phases = 0;  // parity of each stage's next wait
-  bool lost = false;    // a wait ran out
-  while (true) {
-    core.settle(reinterpret_cast<char*>(bufs + Core::kBuf / 16));
-    if constexpr (Core::kQShared) __syncthreads();
+      for (int x = 0; x < Core::kParts; ++x) {
+        const int to_root = warp ^ root_of(x);
+        float4* buf = bufs + (1 - to_root % 2) * (Core::kBuf / 16);
+        __syncthreads();
+        if (to_root >= 2) core.put(buf, x);
+        __syncthreads();
+        if (to_root < 2) core.merge(buf, x, 0);
+        if (to_root == 1) core.put(buf, x);
+        __syncthreads();
+        if (to_root == 0) core.merge(bufs, x, 1);
+      }
+    };
+    int stage = 0;
+    uint32_t phases = 0;  // parity of each stage's next wait
+    bool lost = false;    // a wait ran out
+    while (true) {
+      core.settle(reinterpret_cast<char*>(bufs + Core::kBuf / 16));
+      if constexpr (Core::kQShared) __syncthreads();
 #pragma unroll 1
-    for (int x = 0; x < use.steps; ++x) {
-      const int valid = static_cast<int>(valids >> (5 * (kStages - 1)) & 31);
-      if (valid > 0) {
-        uint64_t* full = &s_full[warp][stage];
-        const uint32_t phase = phases >> stage & 1;
-        if (!warp_wait(full, phase, &s_abort)) {
-          // this or another warp's wait ran out: issue no more, and wait once
-          // more, bounded again, for what is in flight; the status tells
-          lost = done = true;
-          volatile int own = 0;
-          warp_wait(full, phase, &own);
+      for (int x = 0; x < use.steps; ++x) {
+        const int valid = static_cast<int>(valids >> (5 * (kStages - 1)) & 31);
+        if (valid > 0) {
+          uint64_t* full = &s_full[warp][stage];
+          const uint32_t phase = phases >> stage & 1;
+          if (!warp_wait(full, phase, &s_abort)) {
+            // this or another warp's wait ran out: issue no more, and wait once
+            // more, bounded again, for what is in flight; the status tells
+            lost = done = true;
+            volatile int own = 0;
+            warp_wait(full, phase, &own);
+          }
+          phases ^= 1u << stage;
+          const uint32_t at = smem_u32(ring + stage * Core::kStage);
+          core.scores(at, valid);
+          core.values(at, valid);
         }
-        phases ^= 1u << stage;
-        const uint32_t at = smem_u32(ring + stage * Core::kStage);
-        core.scores(at, valid);
-        core.values(at, valid);
+        issue(stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
       }
-      issue(stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
-    }
 
-    const Unit was = use;
-    const long long q_row = q_row_of(was);
-    const bool last = !goes_on(was);
-    if (!last) {  // the next unit's Q, while this one's results are joined
-      next_unit(use);
-      core.fetch(a, q_row_of(use), heads);
-    }
+      const Unit was = use;
+      const long long q_row = q_row_of(was);
+      const bool last = kUnits || !goes_on(alone_c, was);
+      if (!last) {  // the next unit's Q, while this one's results are joined
+        next_unit(alone_c, use);
+        core.fetch(a, q_row_of(use), heads);
+      }
 
-    if constexpr (kAlone) {
+      if constexpr (kAlone) {
 #pragma unroll
-      for (int x = 0; x < Core::kParts; ++x) core.emit(a, q_row, heads, true, 0, x);
-      break;
-    }
-    join_warps();
-    if constexpr (kUnits) {
-      if (a.cluster > 1) {
-        // the CTAs' results: the first CTA's warps take those of up to two CTAs
-        // each, in order of rank, and join theirs
-        const int rank = blockIdx.x % a.cluster;
-        static_assert(Core::kParts * Core::kBuf <= kWarps * kStages * Core::kStage, "ring");
-        float4* all = reinterpret_cast<float4*>(rings);  // every copy has been used
+        for (int x = 0; x < Core::kParts; ++x) core.emit(a, q_row, heads, true, 0, x);
+        if (last) break;
+        continue;
+      }
+      join_warps();
+      if constexpr (kUnits) {
+        if (a.cluster > 1) {
+          // the CTAs' results: the first CTA's warps take those of up to two CTAs
+          // each, in order of rank, and join theirs
+          const int rank = blockIdx.x % a.cluster;
+          static_assert(Core::kParts * Core::kBuf <= kWarps * kStages * Core::kStage, "ring");
+          float4* all = reinterpret_cast<float4*>(rings);  // every copy has been used
+#pragma unroll
+          for (int x = 0; x < Core::kParts; ++x)
+            if (warp == root_of(x)) core.put(all + x * (Core::kBuf / 16), x);
+          cluster_sync();
+          if (rank == 0) {
+            core.clear();
+#pragma unroll 1
+            for (int src = warp; src < a.cluster; src += kWarps)
+#pragma unroll
+              for (int x = 0; x < Core::kParts; ++x)
+                core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x, 0);
+            join_warps();
+          }
+          cluster_sync();  // no CTA ends while its buffers are read
+          if (rank > 0) break;
+        }
 #pragma unroll
         for (int x = 0; x < Core::kParts; ++x)
-          if (warp == root_of(x)) core.put(all + x * (Core::kBuf / 16), x);
-        cluster_sync();
-        if (rank == 0) {
-          core.clear();
-#pragma unroll 1
-          for (int src = warp; src < a.cluster; src += kWarps)
+          if (warp == root_of(x)) core.emit(a, q_row, heads, true, 0, x);
+        break;
+      } else {
+        const int tiles = (was.len + kTile - 1) / kTile;
 #pragma unroll
-            for (int x = 0; x < Core::kParts; ++x)
-              core.merge(in_cluster(all + x * (Core::kBuf / 16), src), x, 0);
-          join_warps();
+        for (int x = 0; x < Core::kParts; ++x)
+          if (warp == root_of(x))
+            core.emit(a, q_row, heads, was.steps == tiles, blockIdx.x * 2ll + (was.t0 == 0 ? 1 : 0),
+                      x);
+        if (warp == 0) {
+          if (lane == 0 && was.t0 == 0 && (a.by_unit || was.steps < tiles)) {
+            // the group of CTAs whose range holds the unit's last tile
+            const unsigned long long past = end - was.left + tiles;
+            const int to = static_cast<int>((past * groups - 1) / total);
+            *split_of(a, was.request, was.head, part) = {was.request, was.head,
+                                                         static_cast<int>(blockIdx.x), to - group};
+          }
         }
-        cluster_sync();  // no CTA ends while its buffers are read
-        if (rank > 0) break;
+        if (last) break;
       }
-#pragma unroll
-      for (int x = 0; x < Core::kParts; ++x)
-        if (warp == root_of(x)) core.emit(a, q_row, heads, true, 0, x);
-      break;
-    } else {
-      const int tiles = (was.len + kTile - 1) / kTile;
-#pragma unroll
-      for (int x = 0; x < Core::kParts; ++x)
-        if (warp == root_of(x))
-          core.emit(a, q_row, heads, was.steps == tiles, blockIdx.x * 2ll + (was.t0 == 0 ? 1 : 0),
-                    x);
-      if (warp == 0) {
-        if (lane == 0 && was.t0 == 0 && (a.by_unit || was.steps < tiles)) {
-          // the group of CTAs whose range holds the unit's last tile
-          const unsigned long long past = end - was.left + tiles;
-          const int to = static_cast<int>((past * groups - 1) / total);
-          *split_of(a, was.request, was.head, part) = {was.request, was.head,
-                                                       static_cast<int>(blockIdx.x), to - group};
-        }
-      }
-      if (last) break;
     }
+    if (bad) atomicExch(a.status, kStatusBadCache);
+    if (lost && lane == 0) atomicExch(a.status, kStatusTimeout);
+  };
+  if constexpr (kWay == kByWarps) {
+    walk(std::true_type());
+  } else {
+    if constexpr (kMaybeAlone)
+      if (alone) return walk(std::true_type());
+    walk(std::false_type());
   }
-  if (bad) atomicExch(a.status, kStatusBadCache);
-  if (lost && lane == 0) atomicExch(a.status, kStatusTimeout);
 }
 
 constexpr int kJoinWarps = 4;
@@ -1154,7 +1219,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   const bool waves = units >= 4 * slots && row_tiles <= 32;
   const bool numbered = tiles + kUnitCost * D.nseq * static_cast<long long>(D.hkv) < 1ll << 31;
   if constexpr (!Core::kQShared) {
-    if (units >= 2 * slots && row_tiles <= 8) {
+    if (units >= kAloneWaves * slots && row_tiles <= kAloneTiles) {
       cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByWarps>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            smem_of<Core>());
@@ -1181,12 +1246,20 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   // By ranges, no more than there can be tiles.
   const unsigned grid = static_cast<unsigned>(max(1ll, min(slots / a.hc, tiles)) * a.hc);
   a.by_unit = units < grid;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByRanges>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_of<Core>());
+  auto launch = [&](auto* kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<Core>());
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
+    return cudaGetLastError();
+  };
+  cudaError_t e;
+  if constexpr (Core::kAloneInRanges)
+    e = units >= kAloneWaves * grid ? launch(&decode_kernel<Core, kByRangesOrWarps>)
+                                    : launch(&decode_kernel<Core, kByRanges>);
+  else
+    e = launch(&decode_kernel<Core, kByRanges>);
   if (e != cudaSuccess) return e;
-  decode_kernel<Core, kByRanges><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(a.by_unit ? static_cast<unsigned>(units) : grid, a.per);

@@ -389,15 +389,27 @@ def test_decode_many_requests(n, dtype):
 
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F3, 128), (F3, 64), (F3, 32)])
 @pytest.mark.parametrize("group", [1, 3, 8, 13])
-def test_decode_many_short_requests(group, dtype, d):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_many_short_requests(group, dtype, d, wide):
     """More units (an odd number of them) than the GPU has room for twice, none longer
-    than a row of the table of 256 (fp32) or 512 tokens: a warp takes each."""
+    than 256 (fp32) or 512 tokens: a warp takes each, and many where the table's rows
+    could hold more."""
     rng = random.Random(group * d)
     longest = 480 if dtype is BF else 230
     lens = [rng.choice((0, 1, 7, 8, 9, 15, 16, 17, 63, 65, 128, 200, longest - 1, longest))
             for _ in range(187)]
     lens[3] = longest
-    _check_decode(*_cache(lens, 7 * group, 7, d, dtype, 16, seed=group))
+    case = _cache(lens, 7 * group, 7, d, dtype, 16, seed=group)
+    _check_decode(*(_wide(*case, 700) if wide else case))
+
+
+@pytest.mark.parametrize("dtype", [BF, F3])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("long", [1, 40, 100])
+def test_decode_more_short_requests_than_warps(dtype, wide, long):
+    rng = random.Random(long)
+    case = _cache([rng.randint(0, long) for _ in range(1100)], 6, 3, 64, dtype, 16)
+    _check_decode(*(_wide(*case, 700) if wide else case))
 
 
 @pytest.mark.parametrize("dtype", [BF, F3])
@@ -408,6 +420,7 @@ def test_decode_many_short_requests_with_bad_pages_and_lengths(dtype):
     table[7, 6] = 1 << 30
     table[9, 0] = kp.shape[0]
     _check_decode(Q, kp, vp, table, lens, status=-1)
+    _check_decode(*_wide(Q, kp, vp, table, lens, 700), status=-1)
     kp.nan_to_num_(), vp.nan_to_num_()       # the whole row of request 188 is read
     lens[10] = -1
     lens[188] = 1 << 30
