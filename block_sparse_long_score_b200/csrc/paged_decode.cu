@@ -31,14 +31,13 @@
 //    share nothing, and the four units of a CTA overlap. For many units of few
 //    tokens, which a CTA would start, join and end for too little (1024 requests of
 //    up to 100 tokens: 45.2 us, 84.1 with a CTA a unit; 512 of up to 250: 49.3 and
-//    57.2; 512 of up to 250 in fp32: 92 and 111; but 256 of up to 1000: 92 and 86,
-//    512 of up to 1000, d = 64: 95 and 87, as the warps that are left at the end
-//    load little). Not where a CTA's warps share Q. Where the table could hold long
-//    requests and there are as many units, the split by ranges looks at the lengths
-//    and gives each warp the units that begin in its own equal range (1024 of up to
-//    100: 57 us, 86 by CTAs' ranges; 512 of up to 130: 42 and 50; 512 of up to 60 in
-//    fp32: 41 and 73; at the bound 800 of up to 250: 91 and 88, 512 of up to 250 with
-//    d = 64: 35 and 39).
+//    57.2, in fp32 92 and 111; but 512 of up to 500: 90 and 87, and of up to 1000,
+//    d = 64: 95 and 87, as the warps that are left at the end load little). Not
+//    where a CTA's warps share Q. Where the table could hold long requests and there
+//    are as many units, the split by ranges looks at the lengths and gives each warp
+//    the units that begin in its own equal range (1024 of up to 100: 57 us, 86 by
+//    CTAs' ranges; 512 of up to 130: 42 and 50; 512 of up to 60 in fp32: 41 and 73; at
+//    the bound 800 of up to 250: 91 and 88, 512 of up to 250 with d = 64: 35 and 39).
 // All work the bounds out on the device from lens, so a captured graph follows
 // the lengths.
 //
@@ -68,9 +67,8 @@ constexpr int kMaxCtas = 640;  // of the split by ranges (bounds the workspace)
 // together (256 requests of up to 500 tokens in a wide table: 66 us; with a cost of
 // 1, 2, 3 tiles a unit 55.7, 54.5, 55.2; 8 of up to 2500: 18.6; 18.0, 17.4, 17.3).
 constexpr int kUnitCost = 2;
-// By warps: no unit of more tiles than this (half of it where the warps' ranges are
-// fixed beforehand, whose ends lie up to a unit apart), and this many units a CTA.
-constexpr int kAloneTiles = 8, kAloneWaves = 2;
+// By warps: no unit of more tokens than this, and so many units a CTA at least.
+constexpr int kAloneTokens = 288, kAloneWaves = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -829,7 +827,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     if (kMaybeAlone) {
       longest = held = 0;
       for (int w = 0; w < kWarps; ++w) longest = max(longest, s_longest[w]), held += s_held[w];
-      alone = longest <= kAloneTiles / 2 * kTile && held * D.hkv >= kAloneWaves * launched;
+      alone = longest <= kAloneTokens && held * D.hkv >= kAloneWaves * launched;
     }
     if (empty) empty_rows<Core>(a, group, launched, part, head0, heads);
     if (!a.by_unit && tid == 0) a.split[blockIdx.x].more = 0;
@@ -1197,8 +1195,8 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   a.sms = num_sms;
   const long long slots = min(num_sms * Core::kCtas, kMaxCtas);  // CTAs the GPU holds
   const long long units = static_cast<long long>(D.nseq) * D.hkv * a.hc;
-  const long long row_tiles =
-      ((static_cast<long long>(D.max_pages) << D.page_shift) + kTile - 1) / kTile;
+  const long long row_tokens = static_cast<long long>(D.max_pages) << D.page_shift;
+  const long long row_tiles = (row_tokens + kTile - 1) / kTile;
   const long long tiles = row_tiles * D.nseq * D.hkv;
   CUtensorMap k_map, v_map;
   if (make_pages_map(&k_map, a.k_pages, D, Core::kBox, Core::kChunk) != XATTN_OK ||
@@ -1210,7 +1208,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
 
-  // By warps: two waves of units or more, of 32 steps of a warp at most.
+  // By warps: many short units.
   // By units: four waves of them, of 32 tiles at most, balance themselves; fewer
   // where the table holds so little that a unit's CTA, or each of its cluster, has
   // eight tiles at most; and where the tiles of all cannot be numbered.
@@ -1219,7 +1217,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   const bool waves = units >= 4 * slots && row_tiles <= 32;
   const bool numbered = tiles + kUnitCost * D.nseq * static_cast<long long>(D.hkv) < 1ll << 31;
   if constexpr (!Core::kQShared) {
-    if (units >= kAloneWaves * slots && row_tiles <= kAloneTiles) {
+    if (units >= kAloneWaves * slots && row_tokens <= kAloneTokens) {
       cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByWarps>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            smem_of<Core>());

@@ -392,10 +392,10 @@ def test_decode_many_requests(n, dtype):
 @pytest.mark.parametrize("wide", [False, True])
 def test_decode_many_short_requests(group, dtype, d, wide):
     """More units (an odd number of them) than the GPU has room for twice, none longer
-    than 256 (fp32) or 512 tokens: a warp takes each, and many where the table's rows
-    could hold more."""
+    than 288 tokens: a warp takes each, and several where the table's rows could hold
+    more."""
     rng = random.Random(group * d)
-    longest = 480 if dtype is BF else 230
+    longest = 270 if not wide else 280
     lens = [rng.choice((0, 1, 7, 8, 9, 15, 16, 17, 63, 65, 128, 200, longest - 1, longest))
             for _ in range(187)]
     lens[3] = longest
