@@ -13,7 +13,7 @@ struct PagedDims {
 
 namespace host {
 
-// 4-D TMA view of a paged cache's K or V (see api.cu).
+// 5-D TMA view of a paged cache's K or V (see api.cu).
 int make_pages_map(CUtensorMap* m, const void* ptr, const PagedDims& D, int box_d,
                    int box_tokens);
 
@@ -49,7 +49,8 @@ inline int check_paged(const xattn_paged* c, bool with_heads, PagedDims* D) {
   const int esize = c->dtype == XATTN_BF16 ? 2 : 4;
   for (long long s : {c->page_stride, c->head_stride, c->token_stride})
     // (a TMA view's strides are below 2^40 bytes)
-    if (s < d || s >= (1ll << 40) || s * esize >= (1ll << 40) || (s * esize) % 16 != 0) return XATTN_ERR_INVALID_ARG;
+    if (s < d || s >= (1ll << 40) || s * esize >= (1ll << 40) || (s * esize) % 16 != 0)
+      return XATTN_ERR_INVALID_ARG;
   D->nseq = nseq;
   D->max_pages = max_pages;
   D->num_pages = c->num_pages;
