@@ -168,7 +168,6 @@ struct CoreBf16 {
   // Q: in registers for up to 8 heads. For more it would take half of them, and
   // sits in shared memory, swizzled like K.
   static constexpr bool kQShared = NT > 1;
-  static constexpr bool kAloneInRanges = !kQShared;  // see decode_kernel
   static constexpr int kQBytes = kQShared ? 8 * NT * kD * 2 : 0;
   static constexpr int kQEach = kQShared ? kQBytes / 16 / (kWarps * 32) : 1;
   uint4 fetched[kQEach];
@@ -416,9 +415,6 @@ struct CoreF32 {
   static constexpr bool kSpread = false;       // (all heads' maxima come with the first)
   static constexpr int kBuf = (kPart * kPieces + 1) * 512;
   static constexpr bool kQShared = false;
-  // (of 8 heads the kernel with both walks takes 74.8 us where the one by CTAs takes
-  // 69.8: 16 requests of up to 16384 tokens, d = 64)
-  static constexpr bool kAloneInRanges = H < 8;
   static constexpr int kQBytes = 0;
   using T = float;
   using F2 = unsigned long long;               // two floats
@@ -705,7 +701,9 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
 
 // How the work is cut (see above). kByRangesOrWarps chooses on the device; it is a
 // kernel of its own since its size costs short calls 0.6 us (5 requests of up to 4001
-// tokens in fp32: 12.2 us, 11.5 without the walk by warps).
+// tokens in fp32: 12.2 us, 11.5 without the walk by warps) and long ones of 8 fp32
+// heads a pass registers (200 of up to 4000 tokens, d = 64: 373 us and 364; where
+// there are as many short units, 512 of up to 50: 39 and 92).
 enum Way { kByRanges, kByRangesOrWarps, kByUnits, kByWarps };
 
 template <class Core, Way kWay>
@@ -1252,7 +1250,7 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
     return cudaGetLastError();
   };
   cudaError_t e;
-  if constexpr (Core::kAloneInRanges)
+  if constexpr (!Core::kQShared)
     e = units >= kAloneWaves * grid ? launch(&decode_kernel<Core, kByRangesOrWarps>)
                                     : launch(&decode_kernel<Core, kByRanges>);
   else
