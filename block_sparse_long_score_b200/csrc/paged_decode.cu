@@ -32,9 +32,8 @@
 //    tokens, which a CTA would start, join and end for too little (1024 requests of
 //    up to 100 tokens: 45.2 us, 84.1 with a CTA a unit; 512 of up to 250: 49.3 and
 //    57.2, in fp32 92 and 111; but 512 of up to 500: 90 and 87, and of up to 1000,
-//    d = 64: 95 and 87, as the warps that are left at the end load little). Not
-//    where a CTA's warps share Q. Where the table could hold long requests and there
-//    are as many units, the split by ranges looks at the lengths and gives each warp
+//    d = 64: 95 and 87, as the warps that are left at the end load little). Where the
+//    table could hold long requests and there are as many units, the split by ranges looks at the lengths and gives each warp
 //    the units that begin in its own equal range (1024 of up to 100: 57 us, 86 by
 //    CTAs' ranges; 512 of up to 130: 42 and 50; 512 of up to 60 in fp32: 41 and 73; at
 //    the bound 800 of up to 250: 91 and 88, 512 of up to 250 with d = 64: 35 and 39).
@@ -210,11 +209,35 @@ struct CoreBf16 {
         const int h = (x * kWarps * 32 + threadIdx.x) / (kD / 8), piece = threadIdx.x % (kD / 8);
         *reinterpret_cast<uint4*>(q_shared + h * (kD * 2) + ((piece ^ h % 8) << 4)) = fetched[x];
       }
-      // ldmatrix: features vary over all four matrices, 32 at a time
-      const uint32_t lane = threadIdx.x % 32;
-      q_at = smem_u32(q_shared) + lane % 8 * (kD * 2) + ((lane / 8 ^ lane % 8) << 4);
+      point_at(q_shared);
     }
     clear();
+  }
+  // ldmatrix of Q: features vary over all four matrices, 32 at a time
+  __device__ __forceinline__ void point_at(const char* q_shared) {
+    const uint32_t lane = threadIdx.x % 32;
+    q_at = smem_u32(q_shared) + lane % 8 * (kD * 2) + ((lane / 8 ^ lane % 8) << 4);
+  }
+  // For one warp by itself, whose Q, where kQShared, has a place of its own (1024
+  // requests of up to 100 tokens, 2 KV heads of 16: 24.7 us, 39.1 by CTAs).
+  __device__ __forceinline__ void settle_alone(const DecodeArgs& a, long long q_row, int heads,
+                                               char* q_own) {
+    if constexpr (kQShared) {
+      const int lane = threadIdx.x % 32;
+      __syncwarp();  // every lane is done with the last unit's
+#pragma unroll 8
+      for (int x = lane; x < kQBytes / 16; x += 32) {
+        const int h = x / (kD / 8), piece = x % (kD / 8);
+        const uint4 y = h < heads ? static_cast<const uint4*>(a.Q)[(q_row + h) * (kD / 8) + piece]
+                                  : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(q_own + h * (kD * 2) + ((piece ^ h % 8) << 4)) = y;
+      }
+      __syncwarp();
+      point_at(q_own);
+      clear();
+    } else {
+      settle(nullptr);
+    }
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -462,6 +485,9 @@ struct CoreF32 {
       for (int j = 0; j < kPairs; ++j) q[h][j] = f2_fma(q[h][j], f2_pack(scale, scale), 0);
     clear();
   }
+  __device__ __forceinline__ void settle_alone(const DecodeArgs&, long long, int, char*) {
+    settle(nullptr);
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int h = 0; h < H; ++h)
@@ -636,10 +662,12 @@ constexpr int stages_of() {
 }
 // Shared memory of a CTA: the warps' rings (on 1024-byte boundaries, as the
 // swizzle wants them), then two buffers of the join; the second is also Q's.
-template <class Core>
+// By warps there is no join, and each has a Q of its own.
+template <class Core, bool kAlone>
 constexpr int smem_of() {
-  return 1024 + kWarps * stages_of<Core>() * Core::kStage + Core::kBuf +
-         (Core::kBuf > Core::kQBytes ? Core::kBuf : Core::kQBytes);
+  constexpr int kJoin = Core::kBuf + (Core::kBuf > Core::kQBytes ? Core::kBuf : Core::kQBytes);
+  constexpr int kOwn = kAlone ? kWarps * Core::kQBytes : 0;
+  return 1024 + kWarps * stages_of<Core>() * Core::kStage + (kJoin > kOwn ? kJoin : kOwn);
 }
 
 // ------------------------------------------------------------ both kernels
@@ -702,8 +730,9 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
 // How the work is cut (see above). kByRangesOrWarps chooses on the device; it is a
 // kernel of its own since its size costs short calls 0.6 us (5 requests of up to 4001
 // tokens in fp32: 12.2 us, 11.5 without the walk by warps) and long ones of 8 fp32
-// heads a pass registers (200 of up to 4000 tokens, d = 64: 373 us and 364; where
-// there are as many short units, 512 of up to 50: 39 and 92).
+// heads a pass, or 32 in bf16, registers (200 of up to 4000 tokens, 8 of 64: 373 us and
+// 364; 800 of up to 4000, 32 of 128: 172.5 and 168.5; where the units are short, 512 of
+// up to 50, 8 of 64: 39 and 92).
 enum Way { kByRanges, kByRangesOrWarps, kByUnits, kByWarps };
 
 template <class Core, Way kWay>
@@ -715,8 +744,6 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
   constexpr int kTile = kWarps * Core::kChunk, kThreads = kWarps * 32;
   constexpr int kStages = stages_of<Core>();
   constexpr bool kMaybeAlone = kWay == kByRangesOrWarps;
-  static_assert(kWay == kByRanges || kWay == kByUnits || !Core::kQShared,
-                "a warp's Q is in its registers");
   const PagedDims& D = a.D;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   // CTAs (clusters) b * hc .. b * hc + hc - 1 take the same tiles for different
@@ -902,7 +929,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     auto q_row_of = [&](const Unit& u) {
       return static_cast<long long>(u.request) * D.hq + u.head * D.group + head0;
     };
-    core.fetch(a, q_row_of(use), heads);
+    if (!kAlone || !Core::kQShared) core.fetch(a, q_row_of(use), heads);
 
     // lane x of a warp holds the page of the warp's step 32 q + x of the unit ahead
     const int per_step = kAlone ? Core::kChunk : kTile;
@@ -978,8 +1005,13 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
     uint32_t phases = 0;  // parity of each stage's next wait
     bool lost = false;    // a wait ran out
     while (true) {
-      core.settle(reinterpret_cast<char*>(bufs + Core::kBuf / 16));
-      if constexpr (Core::kQShared) __syncthreads();
+      if constexpr (kAlone) {
+        core.settle_alone(a, q_row_of(use), heads,
+                          reinterpret_cast<char*>(bufs) + warp * Core::kQBytes);
+      } else {
+        core.settle(reinterpret_cast<char*>(bufs + Core::kBuf / 16));
+        if constexpr (Core::kQShared) __syncthreads();
+      }
 #pragma unroll 1
       for (int x = 0; x < use.steps; ++x) {
         const int valid = static_cast<int>(valids >> (5 * (kStages - 1)) & 31);
@@ -1007,7 +1039,7 @@ __global__ void __launch_bounds__(kWarps * 32, Core::kCtas) decode_kernel(
       const bool last = kUnits || !goes_on(alone_c, was);
       if (!last) {  // the next unit's Q, while this one's results are joined
         next_unit(alone_c, use);
-        core.fetch(a, q_row_of(use), heads);
+        if (!kAlone || !Core::kQShared) core.fetch(a, q_row_of(use), heads);
       }
 
       if constexpr (kAlone) {
@@ -1214,27 +1246,25 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   while (a.cluster < 8 && a.cluster < row_tiles && 2 * a.cluster * units <= slots) a.cluster *= 2;
   const bool waves = units >= 4 * slots && row_tiles <= 32;
   const bool numbered = tiles + kUnitCost * D.nseq * static_cast<long long>(D.hkv) < 1ll << 31;
-  if constexpr (!Core::kQShared) {
-    if (units >= kAloneWaves * slots && row_tokens <= kAloneTokens) {
-      cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByWarps>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           smem_of<Core>());
-      if (e != cudaSuccess) return e;
-      const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
-      decode_kernel<Core, kByWarps><<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
-      return cudaGetLastError();
-    }
+  if (units >= kAloneWaves * slots && row_tokens <= kAloneTokens) {
+    constexpr int kSmem = smem_of<Core, true>();
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByWarps>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
+    decode_kernel<Core, kByWarps><<<grid, kWarps * 32, kSmem, st>>>(a, k_map, v_map);
+    return cudaGetLastError();
   }
   if (waves || row_tiles <= 8 * a.cluster || !numbered) {
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<Core, kByUnits>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_of<Core>());
+                                         smem_of<Core, false>());
     if (e != cudaSuccess) return e;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = a.cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
-    cfg.dynamicSmemBytes = smem_of<Core>();
+    cfg.dynamicSmemBytes = smem_of<Core, false>();
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, decode_kernel<Core, kByUnits>, a, k_map, v_map);
   }
@@ -1242,19 +1272,16 @@ cudaError_t launch_decode(DecodeArgs a, int num_sms, cudaStream_t st) {
   // By ranges, no more than there can be tiles.
   const unsigned grid = static_cast<unsigned>(max(1ll, min(slots / a.hc, tiles)) * a.hc);
   a.by_unit = units < grid;
-  auto launch = [&](auto* kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<Core>());
+  auto launch = [&](auto* kernel, int smem) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kWarps * 32, smem_of<Core>(), st>>>(a, k_map, v_map);
+    kernel<<<grid, kWarps * 32, smem, st>>>(a, k_map, v_map);
     return cudaGetLastError();
   };
-  cudaError_t e;
-  if constexpr (!Core::kQShared)
-    e = units >= kAloneWaves * grid ? launch(&decode_kernel<Core, kByRangesOrWarps>)
-                                    : launch(&decode_kernel<Core, kByRanges>);
-  else
-    e = launch(&decode_kernel<Core, kByRanges>);
+  cudaError_t e = units >= kAloneWaves * grid
+                      ? launch(&decode_kernel<Core, kByRangesOrWarps>, smem_of<Core, true>())
+                      : launch(&decode_kernel<Core, kByRanges>, smem_of<Core, false>());
   if (e != cudaSuccess) return e;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

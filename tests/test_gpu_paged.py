@@ -388,7 +388,7 @@ def test_decode_many_requests(n, dtype):
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F3, 128), (F3, 64), (F3, 32)])
-@pytest.mark.parametrize("group", [1, 3, 8, 13])
+@pytest.mark.parametrize("group", [1, 3, 8, 13, 30])
 @pytest.mark.parametrize("wide", [False, True])
 def test_decode_many_short_requests(group, dtype, d, wide):
     """More units (an odd number of them) than the GPU has room for twice, none longer
