@@ -33,10 +33,11 @@
 //    up to 100 tokens: 45.2 us, 84.1 with a CTA a unit; 512 of up to 250: 49.3 and
 //    57.2, in fp32 92 and 111; but 512 of up to 500: 90 and 87, and of up to 1000,
 //    d = 64: 95 and 87, as the warps that are left at the end load little). Where the
-//    table could hold long requests and there are as many units, the split by ranges looks at the lengths and gives each warp
-//    the units that begin in its own equal range (1024 of up to 100: 57 us, 86 by
-//    CTAs' ranges; 512 of up to 130: 42 and 50; 512 of up to 60 in fp32: 41 and 73; at
-//    the bound 800 of up to 250: 91 and 88, 512 of up to 250 with d = 64: 35 and 39).
+//    table could hold long requests and there are as many units, the split by ranges
+//    looks at the lengths and gives each warp the units that begin in its own equal
+//    range (1024 of up to 100: 57 us, 86 by CTAs' ranges; 512 of up to 130: 42 and 50;
+//    512 of up to 60 in fp32: 41 and 73; at the bound 800 of up to 250: 91 and 88, 512 of
+//    up to 250 with d = 64: 35 and 39).
 // All work the bounds out on the device from lens, so a captured graph follows
 // the lengths.
 //
