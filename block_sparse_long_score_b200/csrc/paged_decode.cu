@@ -146,9 +146,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // 2 % of its rate, and its result back from tensor memory every chunk.
 // ldmatrix brings both operands from TMA's 128-byte swizzle without bank
 // conflicts, V transposed on the way; P goes from the accumulator's layout to an
-// operand's with one 8x8 transpose per 8 tokens. A lane is (r, c) = (lane / 4,
-// lane % 4): tokens r and r + 8 and heads 2c, 2c + 1 of S^T, features r and
-// r + 8 of every 16 of O^T.
+// operand's with an 8x8 transpose per 8 tokens and term. A weight is the sum of two
+// bf16 numbers, so V^T P^T is two products: with one, O of 64 requests of up to 8192
+// tokens is off by 0.0022 of it, with two by 0.0017, which is its rounding to bf16. The
+// second costs up to 16 heads a pass 0 to 4 %, 17 to 32 heads 8 to 17 % (16 requests of
+// up to 65536 tokens, 2 KV heads of 32: 119.6 us and 139.8).
+// A lane is (r, c) = (lane / 4, lane % 4): tokens r and r + 8 and heads 2c, 2c + 1 of
+// S^T, features r and r + 8 of every 16 of O^T.
 template <int kD, int NT>
 struct CoreBf16 {
   static constexpr int kDim = kD;
@@ -171,7 +175,7 @@ struct CoreBf16 {
   static constexpr int kQBytes = kQShared ? 8 * NT * kD * 2 : 0;
   static constexpr int kQEach = kQShared ? kQBytes / 16 / (kWarps * 32) : 1;
   uint4 fetched[kQEach];
-  uint32_t q[NT][kQShared ? 1 : kD / 8], q_at, p[NT][2];
+  uint32_t q[NT][kQShared ? 1 : kD / 8], q_at, p[NT][2], p_low[NT][2];
   float o[NT][kD / 16][4], m[NT][2], base[NT][2], l[NT][2];
   int r, c;
   // This lane's row of the four 8x8 matrices of an ldmatrix, at the first 16
@@ -317,10 +321,24 @@ struct CoreBf16 {
       for (int j = 0; j < 4; ++j) w[j] = ex2(s[t][j] - base[t][j & 1]);
       l[t][0] += w[0] + w[2];
       l[t][1] += w[1] + w[3];
-      // bf16 weights (half a step, 2^-8, relative): what the tensor cores take,
-      // as in the prefill's attention; the sum keeps the fp32 ones
-      p[t][0] = transpose8x8(pack_bf16x2(w[0], w[1]));
-      p[t][1] = transpose8x8(pack_bf16x2(w[2], w[3]));
+      // The tensor cores take bf16: a weight goes to them cut to 8 bits, and what
+      // that leaves, rounded, as a second term; together off by 2^-16 of it at
+      // most. The sum keeps the fp32 one. The second term is above zero (2^-17 of
+      // the weight where nothing is left), so that a value of infinity stays one:
+      // times 0 or times a negative term it would make a NaN.
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float low[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float u = w[2 * x + y];
+          const float cut = __uint_as_float(__float_as_uint(u) & 0xffff0000u);
+          low[y] = fmaxf(u - cut, u * 0x1p-17f);
+        }
+        p[t][x] = transpose8x8(
+            __byte_perm(__float_as_uint(w[2 * x]), __float_as_uint(w[2 * x + 1]), 0x7632));
+        p_low[t][x] = transpose8x8(pack_bf16x2(low[0], low[1]));
+      }
     }
   }
 
@@ -349,8 +367,10 @@ struct CoreBf16 {
         v[0] &= low, v[1] &= low, v[2] &= high, v[3] &= high;
       }
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        mma_bf16(o[t][i], v[0], v[1], v[2], v[3], p_low[t][0], p_low[t][1]);
         mma_bf16(o[t][i], v[0], v[1], v[2], v[3], p[t][0], p[t][1]);
+      }
     }
   }
 
