@@ -16,7 +16,7 @@
 //    whatever the lengths: one long request and many ragged ones load the GPU
 //    alike. A unit inside one CTA's range is written
 //    straight to O; one that several CTAs share leaves a partial result
-//    (running maximum, sum, unnormalised o) in the workspace, at most two a
+//    (the weights' reference, their sum, unnormalised o) in the workspace, at most two a
 //    CTA, and a second kernel, launched with programmatic stream
 //    serialization, joins them in CTA order.
 //  * Units. Each unit goes to a CTA, or to a cluster of CTAs whose results meet
@@ -71,6 +71,7 @@ constexpr int kUnitCost = 2;
 constexpr int kAloneTokens = 288, kAloneWaves = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLead = 8.0f;  // of a weight's reference over the maximum, in powers of two
 
 // What the join has to know of a unit: its first CTA and how many CTAs follow
 // it. One entry per unit, or one per first CTA where there are more units.
@@ -91,7 +92,7 @@ struct DecodeArgs {
   int* status;
   // workspace: per CTA a Split and two partial results of `per` heads
   Split* split;
-  float2* part_ml;  // [CTA][2][per]: maximum (base 2) and sum
+  float2* part_ml;  // [CTA][2][per]: reference of the weights (base 2) and sum
   float* part_o;    // [CTA][2][per][d]
 };
 
@@ -292,15 +293,16 @@ struct CoreBf16 {
         if (r + 8 >= valid) s[t][2] = s[t][3] = -INFINITY;
       }
     }
-    // The reference a weight is taken against lags the true maximum by at most
-    // 2^8: o and l are rescaled only when a logit passes that, which after a
-    // few chunks hardly happens. Weights stay below 2^8, sums in fp32 far from
-    // overflow, and a weight's rounding is relative, so nothing is lost.
+    // The reference m that a weight is taken against is set to kLead above the
+    // maximum so far, and set again (o and l are rescaled) only when a logit passes
+    // it, which after a few chunks hardly happens. So no weight is above 1, the
+    // largest is 2^-kLead at least, and values up to the top of fp32 times a few
+    // such weights stay finite before the division; fp32 holds weights down to
+    // 2^-118 of the largest, and their rounding is relative.
     bool grow = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      grow = grow || fmaxf(s[t][0], s[t][2]) > m[t][0] + 8.0f ||
-             fmaxf(s[t][1], s[t][3]) > m[t][1] + 8.0f;
+      grow = grow || fmaxf(s[t][0], s[t][2]) > m[t][0] || fmaxf(s[t][1], s[t][3]) > m[t][1];
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -310,7 +312,7 @@ struct CoreBf16 {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          rescale(t, x, top);
+          rescale(t, x, top + kLead);
         }
       }
     }
@@ -342,7 +344,7 @@ struct CoreBf16 {
     }
   }
 
-  // Takes the maximum of head (t, x) up to `top`.
+  // Takes the reference of head (t, x) up to `top`.
   __device__ __forceinline__ void rescale(int t, int x, float top) {
     top = fmaxf(top, m[t][x]);
     base[t][x] = top == -INFINITY ? 0.0f : top;
@@ -564,11 +566,11 @@ struct CoreF32 {
       if (kOwn == 2 && g + 4 >= valid) s[kOwn - 1] = -INFINITY;
     }
     float top = kOwn == 2 ? fmaxf(s[0], s[kOwn - 1]) : s[0];
-    if (__any_sync(0xffffffffu, top > m + 8.0f)) {  // as in the bf16 core
+    if (__any_sync(0xffffffffu, top > m)) {  // as in the bf16 core
       if (H < 8) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4 / H));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      top = fmaxf(top, m);
+      top = fmaxf(top + kLead, m);
       base = top == -INFINITY ? 0.0f : top;
       const float f = ex2(m - base);
       m = top;
@@ -1147,7 +1149,7 @@ __device__ __forceinline__ void load_row(const float* p, float (&x)[1]) { x[0] =
 
 // Joins the partial results of a unit for one query head (blockIdx.y). A warp adds
 // every kJoinWarps-th partial's row, in that order; the first rows are read
-// together with the maxima and sums their weights 2^(m - max) come from.
+// together with the references and sums their weights 2^(m - max) come from.
 template <typename T, int kD>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a) {
   constexpr int kPer = kD / 32;  // features a lane

@@ -1,6 +1,6 @@
 """What the decode over a paged cache keeps of its inputs: softmax weights held in
-more bits than the tensors' type, and every token counted once however long a
-request and however the work is cut.
+more bits than the tensors' type, values near the top of the type's range, and
+every token counted once however long a request and however the work is cut.
 
 The reference is the definition in fp64 on the GPU (``_exact``)."""
 import math
@@ -116,6 +116,30 @@ def test_weights_are_held_in_more_bits_than_the_tensors(dtype, d, group, lens, h
     err = (got - O).abs()
     assert bool((err <= tol).all()), f"{(err / tol).max().item():.3g} times its bound"
     assert bool(((got_lse - lse).abs() <= ds + sums + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all())
+
+
+@pytest.mark.parametrize("n,hkv,width", [(1, 1, 0), (1, 1, 2000), (40, 8, 0), (140, 8, 0), (140, 8, 600)])
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_values_near_the_top_of_the_range(dtype, d, n, hkv, width):
+    """One token of 80 has two thirds of the weight, far above the tokens before it, and every
+    value is 1e38: O is 1e38, although weights above 3.4 times it are no longer finite."""
+    lens = [80] * n
+    table, N = _table(lens, 16, width=width)
+    kp = torch.zeros(N, hkv, 16, d, device=DEV, dtype=dtype)
+    vp = torch.full_like(kp, 1e38)
+    for i in range(n):
+        kp[table[i, 70 // 16], :, 70 % 16, 3] = 5.0 * math.sqrt(d)
+    Q = torch.zeros(n, 4 * hkv, d, device=DEV, dtype=dtype)
+    Q[..., 3] = 1.0
+    got, lse = _decode(Q, kp, vp, table, _i32(lens))
+    # O: half a step, twice (of the weights' sum and of O), and 100 fp32 steps on the way
+    want = vp[0, 0, 0, 0].double()
+    half = R.BF16_HALF if dtype == BF else R.F32_HALF
+    assert bool(((got - want).abs() <= want * (half + 2.0 ** -16 + 100 * 2.0 ** -23)).all())
+    # lse: base-2 terms of up to 16 (a scale, a product, a maximum), natural ones of up to 11 and 6,
+    # an exponential: some 60 steps of 2^-23 and 2^-21
+    key = kp[table[0, 4], 0, 6, 3].double().item() / math.sqrt(d)
+    assert bool(((lse - math.log(79 + math.exp(key))).abs() <= 2.0 ** -16).all())
 
 
 def _marked_pages(N, hkv, page, d, dtype, seed):
