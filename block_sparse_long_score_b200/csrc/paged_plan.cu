@@ -183,7 +183,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
     // pages given back
     for (int x = s_back[0] + me; x < s_back[n]; x += all) {
       const int i = find(s_back, n, x);
-      ring_at(free_pages + x) = a.table[static_cast<long long>(i0 + i) * a.max_pages + x - s_back[i]];
+      const int page = a.table[static_cast<long long>(i0 + i) * a.max_pages + x - s_back[i]];
+      bad_page = bad_page || page < 0 || page >= a.num_pages;
+      ring_at(free_pages + x) = page;
     }
     // slots, a token a thread, whose reads of page ids overlap four at a time;
     // from the last thread on, as the first ones have more of the pages

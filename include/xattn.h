@@ -464,7 +464,8 @@ typedef struct {
  * free pages; XATTN_ERR_INVALID_ARG when fresh < -1, lens < 0, a row would
  * exceed max_pages, the new tokens exceed max_tokens, or pool is not the
  * state of a ring of num_pages entries. A ring or table entry that is no page
- * gives its tokens the slot -1 and is reported as XATTN_ERR_INVALID_ARG.
+ * gives its tokens the slot -1, or goes to the ring as it is (and counts as a page
+ * there) when its request ends; both are reported as XATTN_ERR_INVALID_ARG.
  * A page belongs to one row: rows that share pages cannot both end.
  * Errors: INVALID_ARG (NULL pointer, a size below 1, max_tokens < 0),
  * UNSUPPORTED (page_size, num_pages * page_size above 2^31 - 1, max_pages *
