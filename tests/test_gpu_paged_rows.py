@@ -1,16 +1,34 @@
-"""The paged cache as a server holds it: entries that are no pages."""
+"""The paged cache as a server holds it: rows that wait between the busy ones, and entries
+that are no pages."""
 import pytest
 import torch
 
-from block_sparse_long_score_b200 import xattn_get_device_status, xattn_paged_plan
+from block_sparse_long_score_b200 import (xattn_get_device_status, xattn_paged_append,
+                                          xattn_paged_plan)
+from tests import paged_ref as R
 
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
+BF = torch.bfloat16
 
 
 def _i32(v):
     return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _us(call, times=5):
+    """Least device time of a call, in microseconds."""
+    call()
+    best = float("inf")
+    for _ in range(times):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1000)
+    return best
 
 
 # ------------------------------------------------------------------ plan
@@ -32,3 +50,65 @@ def test_plan_reports_what_an_ended_request_gives_back(n, bad):
     assert out[0].tolist() == [0, 16, 6] + [0] * fill and out[1].tolist() == [8, 5]
     assert out[2].tolist() == [0, 0, 0, 1] + [1] * fill and out[3].tolist() == [37, -1]
     assert t[3].tolist() == [6, 3, bad, 0, 0, 0, 0, 0, 4, 5] and t[4].tolist() == table
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("starts,kept", [([0, 4, 2], []), ([0, 2, 9], [0, 1]), ([-3, 2, 3], [2]),
+                                         ([1, 2, 3], [1, 2])])
+def test_append_leaves_out_what_broken_starts_misplace(starts, kept):
+    """Tokens of a request whose starts are no prefix sum over K's rows are reported and left
+    out; the others land where they belong."""
+    kp, vp = (torch.full((4, 1, 16, 64), -9.0, device=DEV) for _ in range(2))
+    K = torch.arange(3.0 * 64, device=DEV).reshape(3, 64)
+    want_k, want_v = kp.clone(), vp.clone()
+    for t in kept:
+        want_k[0, 0, 5 + t], want_v[0, 0, 5 + t] = K[t], K[t] + 1000
+    xattn_paged_append(K, K + 1000, _i32([5, 6, 7]), kp, vp, starts=_i32(starts))
+    torch.cuda.synchronize()
+    assert xattn_get_device_status() == -1
+    assert torch.equal(kp, want_k) and torch.equal(vp, want_v)
+
+
+def _prompts(n, rows, lens, hkv, d, dtype):
+    """K, V, slots, starts and pages of prompts that enter the given rows of n."""
+    T, page = sum(lens), 16
+    g = torch.Generator(device=DEV).manual_seed(T)
+    N = R.pages(T, page) + 1
+    slots = torch.randperm(N * page, device=DEV, generator=g)[:T].to(torch.int32)
+    K, V = (torch.randn(T * hkv, d, device=DEV, generator=g).to(dtype) for _ in range(2))
+    grow = torch.zeros(n + 1, dtype=torch.int64, device=DEV)
+    for r, L in zip(rows, lens):
+        grow[r + 1] = L
+    kp, vp = (torch.zeros(N, hkv, page, d, device=DEV, dtype=dtype) for _ in range(2))
+    return K, V, slots, grow.cumsum(0).to(torch.int32), kp, vp
+
+
+@pytest.mark.parametrize("n,rows,lens", [
+    (65536, (0, 65535), (601, 1200)), (65536, (7, 8, 40000), (1000, 1, 999)),
+    (5000, (0, 1, 2, 3, 4997, 4999), (1, 300, 2, 1700, 33, 1201)), (33, (31, 32), (5000, 4100)),
+    (1 << 20, (3, (1 << 20) - 1), (4001, 6001))])
+def test_append_finds_its_rows_among_idle_ones(n, rows, lens):
+    hkv, d = 2, 64
+    K, V, slots, starts, kp, vp = _prompts(n, rows, lens, hkv, d, BF)
+    want_k, want_v, at, page = kp.clone(), vp.clone(), 0, 16
+    for L in lens:
+        s = slots[at:at + L].long()
+        for want, x in ((want_k, K), (want_v, V)):
+            want[s // page, :, s % page] = \
+                x[at * hkv:(at + L) * hkv].reshape(hkv, L, d).transpose(0, 1)
+        at += L
+    xattn_paged_append(K, V, slots, kp, vp, starts=starts)
+    torch.cuda.synchronize()
+    assert xattn_get_device_status() == 0
+    assert torch.equal(kp, want_k) and torch.equal(vp, want_v)
+
+
+def test_append_does_not_walk_the_idle_rows():
+    """Two prompts in the first and last of 65536 rows take about the time that they take
+    in the first two; a CTA holds tokens of both (the first prompt's length is odd)."""
+    n = 65536
+    near, far = (_prompts(n, rows, (1201, 2000), 2, 64, BF) for rows in ((0, 1), (0, n - 1)))
+    us = [_us(lambda: xattn_paged_append(x[0], x[1], x[2], x[4], x[5], starts=x[3]))
+          for x in (near, far)]
+    assert us[1] < 3 * us[0] + 20, us
