@@ -4,13 +4,13 @@ import pytest
 import torch
 
 from block_sparse_long_score_b200 import (xattn_get_device_status, xattn_paged_append,
-                                          xattn_paged_plan)
+                                          xattn_paged_decode, xattn_paged_plan)
 from tests import paged_ref as R
 
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
-BF = torch.bfloat16
+BF, F3 = torch.bfloat16, torch.float32
 
 
 def _i32(v):
@@ -112,3 +112,70 @@ def test_append_does_not_walk_the_idle_rows():
     us = [_us(lambda: xattn_paged_append(x[0], x[1], x[2], x[4], x[5], starts=x[3]))
           for x in (near, far)]
     assert us[1] < 3 * us[0] + 20, us
+
+
+# ---------------------------------------------------------------- decode
+
+def _busy(n, rows, lens, hq, hkv, d, dtype, width):
+    g = torch.Generator(device=DEV).manual_seed(n)
+    page = 16
+    have = [R.pages(x, page) for x in lens]
+    N = sum(have) + 1
+    kp, vp = (torch.randn(N, hkv, page, d, device=DEV, generator=g).to(dtype) for _ in range(2))
+    perm = torch.randperm(N, device=DEV, generator=g).to(torch.int32)
+    table = torch.full((n, width), -1, dtype=torch.int32, device=DEV)
+    L, at = torch.zeros(n, dtype=torch.int32, device=DEV), 0
+    for r, size, h in zip(rows, lens, have):
+        table[r, :h] = perm[at:at + h]
+        L[r] = size
+        at += h
+    return torch.randn(n, hq, d, device=DEV, generator=g).to(dtype), kp, vp, table, L
+
+
+@pytest.mark.parametrize("n,rows,lens", [
+    (20000, (0, 19999), (9000, 9000)), (4096, (0, 31, 32, 33, 64, 97, 4000), (700,) * 7),
+    (4096, tuple(range(5, 4096, 61)), tuple(range(1, 69))), (130, (0, 129), (3000, 1)),
+    (3000, (2999,), (5000,)), (100, (1, 34, 67, 99), (2000, 90, 700, 1))])
+@pytest.mark.parametrize("dtype,hq,hkv,d", [(BF, 8, 2, 64), (BF, 32, 2, 128), (F3, 4, 2, 32)])
+def test_decode_of_few_busy_rows_among_idle_ones(n, rows, lens, dtype, hq, hkv, d):
+    Q, kp, vp, table, L = _busy(n, rows, lens, hq, hkv, d, dtype, 600)
+    O, lse = xattn_paged_decode(Q, kp, vp, table, L, lse=True)
+    torch.cuda.synchronize()
+    assert xattn_get_device_status() == 0
+    busy = torch.tensor(rows, device=DEV)
+    want, L64, tol, tol_lse = R.decode(Q[busy], kp, vp, table[busy], L[busy])
+    assert bool(((O[busy].cpu().double() - want).abs() <= tol).all())
+    assert bool(((lse[busy].cpu().double() - L64).abs() <= tol_lse).all())
+    idle = L == 0
+    assert bool((O[idle] == 0).all()) and bool((lse[idle] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F3])
+def test_decode_of_many_short_busy_rows_far_apart(dtype):
+    """Enough short requests for the split by warps, idle rows between them."""
+    n = 20000
+    rows = list(range(3, n, 29))
+    lens = [1 + (11 * i) % 60 for i in range(len(rows))]
+    Q, kp, vp, table, L = _busy(n, rows, lens, 8, 4, 64, dtype, 40)
+    O, lse = xattn_paged_decode(Q, kp, vp, table, L, lse=True)
+    torch.cuda.synchronize()
+    assert xattn_get_device_status() == 0
+    busy = torch.tensor(rows, device=DEV)
+    want, L64, tol, tol_lse = R.decode(Q[busy], kp, vp, table[busy], L[busy])
+    assert bool(((O[busy].cpu().double() - want).abs() <= tol).all())
+    assert bool(((lse[busy].cpu().double() - L64).abs() <= tol_lse).all())
+    assert bool((O[L == 0] == 0).all()) and bool((lse[L == 0] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F3])
+def test_decode_does_not_walk_the_idle_rows(dtype):
+    """Requests spread over 65536 rows take about the time that they take in the first ones;
+    their lengths put ends of units inside CTAs' ranges. A CTA's range crosses one gap of 8190 rows
+    at most, and two walks of it, 128 rows a step, are 2 x 64 dependent reads of 1 us at the
+    very most; row by row they are 2 x 8190 reads, 800 us as measured. (The scan of the lengths,
+    512 rows a thread, differs by up to 50 us itself.)"""
+    n, lens = 65536, [14000 + 331 * i for i in range(9)]
+    near, far = (_busy(n, rows, lens, 8, 2, 64, dtype, 1100)
+                 for rows in (range(9), range(0, n, n // 8 - 1)))
+    us = [_us(lambda: xattn_paged_decode(*x)) for x in (near, far)]
+    assert us[1] < us[0] + 128 + 50, us
