@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from .pipeline import prefill_attention
-from .xattn import (make_paged, xattn_paged_append, xattn_paged_decode,
+from .xattn import (_append_call, _call_on, _decode_call, make_paged,
                     xattn_paged_decode_workspace_bytes, xattn_paged_plan, xattn_prefill_varlen)
 
 __all__ = ["PagedCache", "plan_buffers", "decode_buffers"]
@@ -44,12 +44,21 @@ def decode_buffers(Q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor) 
     }
 
 
+def _aligned(*tensors: torch.Tensor) -> None:
+    """The library refuses a tensor that does not start on a 16-byte boundary; here it has
+    to be known before the plan is made."""
+    for t in tensors:
+        if t.data_ptr() % 16:
+            raise ValueError("a tensor does not start on a 16-byte boundary")
+
+
 class PagedCache:
     """Keys and values of up to ``nseq`` requests in ``num_pages`` pages.
 
     A step that would need more pages than are free enters nothing: lengths and
     tables stay as they are, the attention sees the tokens there were, and
-    xattn_get_device_status returns XATTN_ERR_PAGES.
+    xattn_get_device_status returns XATTN_ERR_PAGES. A call that is refused on the host
+    (ValueError, XattnError) changes nothing either.
 
     Attributes (device tensors, all updated in place, so a captured CUDA graph
     stays valid): ``k_pages``, ``v_pages`` [num_pages, hkv, page_size, d];
@@ -81,9 +90,17 @@ class PagedCache:
         the cache. Q: [batch, hq, L, d], K, V: [batch, hkv, L, d]; ``fresh`` is
         L for each of the ``batch`` rows that take a prompt, in order, and 0
         elsewhere. Returns O."""
-        starts, slots = self.plan(fresh, buffers)
-        xattn_paged_append(K, V, slots, self.k_pages, self.v_pages, starts=starts)
-        return prefill_attention(Q, K, V, B, S, tau, causal)
+        append = self._append_prompts(K, V, buffers)
+        O = prefill_attention(Q, K, V, B, S, tau, causal)
+        self.plan(fresh, buffers)
+        _call_on(*append)
+        return O
+
+    def _append_prompts(self, K, V, buffers) -> tuple:
+        append = _append_call(K, V, buffers["slots"], self.k_pages, self.v_pages,
+                              buffers["starts"])
+        _aligned(K, V)
+        return append
 
     def prefill_varlen(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seqlens, hq: int,
                        B: int, S: int, tau, causal: bool, fresh: torch.Tensor,
@@ -91,10 +108,11 @@ class PagedCache:
         """As ``prefill``, for prompts of different lengths packed as
         xattn_prefill_varlen takes them; ``seqlens`` are the lengths (host) of
         the rows with ``fresh`` > 0, in order."""
-        starts, slots = self.plan(fresh, buffers)
-        xattn_paged_append(K, V, slots, self.k_pages, self.v_pages, starts=starts)
-        return xattn_prefill_varlen(Q, K, V, seqlens, hq, self.k_pages.shape[1], B, S, causal,
-                                    tau)
+        append = self._append_prompts(K, V, buffers)
+        O = xattn_prefill_varlen(Q, K, V, seqlens, hq, self.k_pages.shape[1], B, S, causal, tau)
+        self.plan(fresh, buffers)
+        _call_on(*append)
+        return O
 
     def step(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, fresh: torch.Tensor,
              buffers: dict, lse: Optional[bool] = None):
@@ -105,8 +123,21 @@ class PagedCache:
         the last new token are left out). ``buffers`` holds plan_buffers' and
         decode_buffers' entries. Rows of requests without a new token attend
         to what they have. Returns O, or (O, lse)."""
-        _, slots = self.plan(fresh, buffers)
-        xattn_paged_append(K, V, slots, self.k_pages, self.v_pages)
-        return xattn_paged_decode(Q, self.k_pages, self.v_pages, self.table, self.lens,
-                                  out=buffers["out"], lse=buffers["lse"] if lse else None,
-                                  workspace=buffers["ws"])
+        append = _append_call(K, V, buffers["slots"], self.k_pages, self.v_pages, None)
+        decode, out, row_lse, ws = _decode_call(Q, self.k_pages, self.v_pages, self.table,
+                                                self.lens, buffers["out"],
+                                                buffers["lse"] if lse else None, buffers["ws"])
+        _aligned(Q, K, V, out, ws)
+        tokens, hkv, d = K.shape
+        if tokens > 1 and not (hkv * d <= K.stride(0) <= 1 << 31
+                               and K.stride(0) * K.element_size() % 16 == 0):
+            raise ValueError("the tokens of K and V must not overlap and lie a multiple of 16 "
+                             "bytes apart")
+        need = xattn_paged_decode_workspace_bytes(
+            make_paged(self.k_pages, Q.shape[1], Q.shape[0], self.table.shape[1]))
+        if need == 0 or ws.nbytes < need:
+            raise ValueError("the heads do not fit the cache, or the workspace is too small")
+        self.plan(fresh, buffers)
+        _call_on(*append)
+        _call_on(*decode)
+        return out if row_lse is None else (out, row_lse)

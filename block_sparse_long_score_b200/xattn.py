@@ -763,6 +763,11 @@ def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
     ``starts`` (int32 [nseq + 1]), they are request after request, each a
     contiguous [hkv, L_i, d] array: the packed layout of xattn_prefill_varlen,
     or [batch, hkv, L, d] tensors; they hold len(slots) tokens' rows."""
+    _call_on(*_append_call(K, V, slots, k_pages, v_pages, starts))
+
+
+def _append_call(K, V, slots, k_pages, v_pages, starts) -> tuple:
+    """What xattn_paged_append hands to _call_on, after its checks."""
     dev, dtype = _device_of(k_pages, "k_pages"), k_pages.dtype
     s_shape, p_shape = slots.shape, k_pages.shape
     if len(s_shape) != 1 or len(p_shape) != 4:
@@ -789,10 +794,10 @@ def xattn_paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
         if nseq < 1 or K.numel() != rows or V.numel() != rows:
             raise ValueError("with starts, K and V must hold len(slots) * hkv rows of d")
     shape = _paged_pair(k_pages, v_pages, 1, nseq, 1, dev)
-    _call_on(dev, "xattn_paged_append", K.data_ptr(), V.data_ptr(), ctypes.byref(shape), tokens,
-             XATTN_TOKEN_MAJOR if starts is None else XATTN_HEAD_MAJOR, stride,
-             _ready(slots, "slots", dev, torch.int32), first, k_pages.data_ptr(),
-             v_pages.data_ptr())
+    return (dev, "xattn_paged_append", K.data_ptr(), V.data_ptr(), ctypes.byref(shape), tokens,
+            XATTN_TOKEN_MAJOR if starts is None else XATTN_HEAD_MAJOR, stride,
+            _ready(slots, "slots", dev, torch.int32), first, k_pages.data_ptr(),
+            v_pages.data_ptr())
 
 
 def xattn_paged_decode_workspace_bytes(shape: _Paged) -> int:
@@ -808,6 +813,14 @@ def xattn_paged_decode(Q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     [nseq, hq, d] (or [nseq, hq, 1, d]); pages [num_pages, hkv, page_size, d];
     table int32 [nseq, max_pages]; lens int32 [nseq]. Returns O like Q, or (O,
     lse [nseq, hq]) if lse is True or a tensor."""
+    call, out, lse, workspace = _decode_call(Q, k_pages, v_pages, table, lens, out, lse, workspace)
+    _call_on(*call)
+    return out if lse is None else (out, lse)
+
+
+def _decode_call(Q, k_pages, v_pages, table, lens, out, lse, workspace) -> tuple:
+    """What xattn_paged_decode hands to _call_on, after its checks, and the tensors that the
+    call writes to (out, lse or None, workspace)."""
     dev, dtype, q_shape, t_shape = _device_of(Q, "Q"), k_pages.dtype, Q.shape, table.shape
     if len(q_shape) != 3 and (len(q_shape) != 4 or q_shape[2] != 1):
         raise ValueError("Q must be [nseq, hq, d] or [nseq, hq, 1, d]")
@@ -832,12 +845,12 @@ def xattn_paged_decode(Q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     if workspace is None:
         workspace = torch.empty(max(xattn_paged_decode_workspace_bytes(shape), 1),
                                 device=Q.device, dtype=torch.uint8)
-    _call_on(dev, "xattn_paged_decode", _ready(Q, "Q", dev, dtype), k_pages.data_ptr(),
-             v_pages.data_ptr(), ctypes.byref(shape), _ready(table, "table", dev, torch.int32),
-             _ready(lens, "lens", dev, torch.int32), _ready(out, "O", dev, dtype),
-             None if lse is None else _ready(lse, "lse", dev, torch.float32),
-             _ready(workspace, "workspace", dev, workspace.dtype), workspace.nbytes)
-    return out if lse is None else (out, lse)
+    call = (dev, "xattn_paged_decode", _ready(Q, "Q", dev, dtype), k_pages.data_ptr(),
+            v_pages.data_ptr(), ctypes.byref(shape), _ready(table, "table", dev, torch.int32),
+            _ready(lens, "lens", dev, torch.int32), _ready(out, "O", dev, dtype),
+            None if lse is None else _ready(lse, "lse", dev, torch.float32),
+            _ready(workspace, "workspace", dev, workspace.dtype), workspace.nbytes)
+    return call, out, lse, workspace
 
 
 def xattn_selftest_timeout(device=None) -> None:

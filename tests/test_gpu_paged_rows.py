@@ -1,10 +1,12 @@
-"""The paged cache as a server holds it: rows that wait between the busy ones, and entries
-that are no pages."""
+"""The paged cache as a server holds it: rows that wait between the busy ones, entries
+that are no pages, and calls that are refused."""
 import pytest
 import torch
 
-from block_sparse_long_score_b200 import (xattn_get_device_status, xattn_paged_append,
+from block_sparse_long_score_b200 import (PagedCache, XattnError, decode_buffers, plan_buffers,
+                                          xattn_get_device_status, xattn_paged_append,
                                           xattn_paged_decode, xattn_paged_plan)
+from block_sparse_long_score_b200.synth import make_problem
 from tests import paged_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +181,65 @@ def test_decode_does_not_walk_the_idle_rows(dtype):
                  for rows in (range(9), range(0, n, n // 8 - 1)))
     us = [_us(lambda: xattn_paged_decode(*x)) for x in (near, far)]
     assert us[1] < us[0] + 128 + 50, us
+
+
+# -------------------------------------------------------------- refusals
+
+def _state(c):
+    return [x.clone() for x in (c.lens, c.pool, c.table, c.ring)]
+
+
+def _unchanged(c, before):
+    torch.cuda.synchronize()
+    return all(torch.equal(x, y) for x, y in zip(_state(c), before))
+
+
+def test_a_refused_step_enters_nothing():
+    c = PagedCache(2, 4, 8, 16, 2, 128, BF, DEV)
+    Q = torch.randn(2, 8, 128, device=DEV).to(BF)
+    K, V = (torch.randn(2, 2, 128, device=DEV).to(BF) for _ in range(2))
+    buf = {**plan_buffers(c.table, 2), **decode_buffers(Q, c.k_pages, c.table)}
+    fresh = _i32([1, 1])
+    c.step(Q, K, V, fresh, buf)
+    before = _state(c)
+    shifted = torch.empty(2 * 2 * 128 + 4, device=DEV, dtype=BF)[4:].view(2, 2, 128)
+    stride = torch.empty(2, 2 * 128 + 4, device=DEV, dtype=BF)[:, :256].unflatten(1, (2, 128))
+    odd_q = torch.empty(2 * 8 * 128 + 4, device=DEV, dtype=BF)[4:].view(2, 8, 128)
+    for q, k, v, b in ((Q, K[:1], V, buf), (Q, K.float(), V, buf), (Q, K, V.cpu(), buf),
+                       (Q[:1], K, V, buf), (Q.float(), K, V, buf), (Q[..., :64], K, V, buf),
+                       (Q, shifted, V, buf), (Q, K, shifted, buf), (Q, stride, stride, buf),
+                       (odd_q, K, V, buf), (Q, K, V, {**buf, "out": buf["out"][:1]}),
+                       (Q, K, V, {**buf, "out": odd_q}), (Q, K, V, {**buf, "ws": buf["ws"][:64]}),
+                       (Q, K, V, {**buf, "ws": buf["ws"][8:]}),
+                       (Q, K, V, {**buf, "lse": buf["lse"][:, :4]}),
+                       (torch.zeros(2, 7, 128, device=DEV, dtype=BF), K, V,
+                        {**buf, "out": torch.zeros(2, 7, 128, device=DEV, dtype=BF),
+                         "lse": buf["lse"][:, :7].contiguous()})):
+        with pytest.raises((ValueError, XattnError)):
+            c.step(q, k, v, fresh, b, lse=True)
+        assert _unchanged(c, before)
+    c.step(Q, K, V, fresh, buf)
+    assert c.lens.tolist() == [2, 2] and xattn_get_device_status() == 0
+
+
+def test_a_refused_prefill_enters_nothing():
+    p = make_problem("c1", L=1024, hq=8, hkv=2, seed=3)
+    Q, K, V = (x.contiguous().to(DEV) for x in (p.Q, p.K, p.V))
+    tau = p.tau.tolist()
+    c = PagedCache(2, 20, 40, 128, 2, 128, BF, DEV)
+    before, fresh = _state(c), _i32([1024, 0])
+    buf, large = plan_buffers(c.table, 1024), plan_buffers(c.table, 2048)
+    for q, k, v, B, t, b in ((Q, K, V, p.B, tau, large), (Q, K, V[:, :1], p.B, tau, buf),
+                             (Q, K, V, 100, tau, buf), (Q, K, V, p.B, [2.0] * 8, buf),
+                             (Q, K, V, p.B, tau[:3], buf), (Q[:, :7], K, V, p.B, tau, buf),
+                             (Q, K.float(), V.float(), p.B, tau, buf)):
+        with pytest.raises((ValueError, XattnError)):
+            c.prefill(q, k, v, B, p.S, t, p.causal, fresh, b)
+        assert _unchanged(c, before)
+    flat = [x[0].reshape(-1, 128) for x in (Q, K, V)]
+    for seqlens, t, b in (([1024], tau, large), ([1000], tau, buf), ([1024], [0.0] * 8, buf)):
+        with pytest.raises((ValueError, XattnError)):
+            c.prefill_varlen(*flat, seqlens, 8, p.B, p.S, t, p.causal, fresh, b)
+        assert _unchanged(c, before)
+    c.prefill(Q, K, V, p.B, p.S, tau, p.causal, fresh, buf)
+    assert c.lens.tolist() == [1024, 0] and xattn_get_device_status() == 0
