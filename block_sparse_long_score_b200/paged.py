@@ -89,7 +89,8 @@ class PagedCache:
         """Sparse prefill attention of new prompts, whose keys and values enter
         the cache. Q: [batch, hq, L, d], K, V: [batch, hkv, L, d]; ``fresh`` is
         L for each of the ``batch`` rows that take a prompt, in order, and 0
-        elsewhere. Returns O."""
+        elsewhere. Inside a CUDA-graph capture ``tau`` has to be a CUDA tensor.
+        Returns O."""
         append = self._append_prompts(K, V, buffers)
         O = prefill_attention(Q, K, V, B, S, tau, causal)
         self.plan(fresh, buffers)

@@ -1,11 +1,12 @@
 """The paged cache as a server holds it: rows that wait between the busy ones, entries
-that are no pages, and calls that are refused."""
+that are no pages, and calls that are refused or captured."""
 import pytest
 import torch
 
 from block_sparse_long_score_b200 import (PagedCache, XattnError, decode_buffers, plan_buffers,
-                                          xattn_get_device_status, xattn_paged_append,
-                                          xattn_paged_decode, xattn_paged_plan)
+                                          prefill_attention, xattn_get_device_status,
+                                          xattn_paged_append, xattn_paged_decode,
+                                          xattn_paged_plan)
 from block_sparse_long_score_b200.synth import make_problem
 from tests import paged_ref as R
 
@@ -183,7 +184,7 @@ def test_decode_does_not_walk_the_idle_rows(dtype):
     assert us[1] < us[0] + 128 + 50, us
 
 
-# -------------------------------------------------------------- refusals
+# ----------------------------------------------------- refusals, capture
 
 def _state(c):
     return [x.clone() for x in (c.lens, c.pool, c.table, c.ring)]
@@ -243,3 +244,34 @@ def test_a_refused_prefill_enters_nothing():
         assert _unchanged(c, before)
     c.prefill(Q, K, V, p.B, p.S, tau, p.causal, fresh, buf)
     assert c.lens.tolist() == [1024, 0] and xattn_get_device_status() == 0
+
+
+def test_a_captured_prefill_takes_new_prompts():
+    """A prefill captured with thresholds on the device and replayed: other prompts into other
+    rows, the first ones ended in between."""
+    p = make_problem("c1", L=1024, hq=8, hkv=2, seed=3)
+    Q, K, V = (x.contiguous().to(DEV) for x in (p.Q, p.K, p.V))
+    tau = torch.from_numpy(p.tau).to(DEV)
+    c = PagedCache(3, 9, 20, 128, 2, 128, BF, DEV)
+    fresh = _i32([0, 0, 0])
+    buf = plan_buffers(c.table, 1024)
+    c.prefill(Q, K, V, p.B, p.S, tau, p.causal, fresh, buf)      # nothing new: the warm-up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O = c.prefill(Q, K, V, p.B, p.S, tau, p.causal, fresh, buf)
+    end = plan_buffers(c.table, 0)
+    for turn, (row, ended) in enumerate(((1, None), (0, 1), (2, 0), (1, 2))):
+        if ended is not None:
+            c.plan(_i32([-1 if i == ended else 0 for i in range(3)]), end)
+        for dst in (Q, K, V):
+            dst.copy_(dst.flip(2))
+        fresh.copy_(_i32([1024 if i == row else 0 for i in range(3)]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert xattn_get_device_status() == 0
+        assert torch.equal(O, prefill_attention(Q, K, V, p.B, p.S, tau, p.causal)), turn
+        assert c.lens[row].item() == 1024 and c.lens.sum().item() == 1024
+        for pages, src in ((c.k_pages, K), (c.v_pages, V)):
+            got = pages[c.table[row, :8].long()].transpose(0, 1).reshape(2, 1024, 128)
+            assert torch.equal(got, src[0])
