@@ -6,8 +6,8 @@
 // K and V are read once, which bounds the call: 2 * d * esize bytes a token
 // against 4 * g * d flops, g flops a byte in bf16 (26 TFLOP/s at the measured
 // copy rate for g = 4). Measured, 32 query and 8 KV heads of 128 in bf16: one
-// request of 131072 tokens 87.4 us (6.1 TB/s, 94 % of the copy rate), 64 of up to
-// 8192 161 us (95 %), one of 517 8.4 us.
+// request of 131072 tokens 87.0 us (6.2 TB/s, 94 % of the copy rate), 64 of up to
+// 8192 161 us (95 %), one of 517 8.6 us.
 //
 // Work split. A unit is a request's KV head; its tokens are cut into tiles of
 // kWarps * kChunk. Three ways, chosen on the host by what the table can hold:
@@ -22,22 +22,22 @@
 //  * Units. Each unit goes to a CTA, or to a cluster of CTAs whose results meet
 //    through distributed shared memory: one launch, no scan of the lengths and
 //    no workspace. For tables of so few tokens that latency is all (one request
-//    of 517 tokens: 8.4 us, 10.5 in ranges), and for many more units than the GPU
+//    of 517 tokens: 8.6 us, 9.8 in ranges), and for many more units than the GPU
 //    has room for, which the block scheduler balances (256 requests of up to 500
-//    tokens, 8 KV heads: 49.1 us, 54.5 in ranges; of up to 2000: 159.6 and 169);
+//    tokens, 8 KV heads: 49.4 us, 55.2 in ranges; of up to 2000: 161.6 and 168.8);
 //    the latter only where no unit can be long, as one CTA would be left with it
-//    (60000 tokens among 255 x 200: 632 us by units, 82 in ranges).
+//    (60000 tokens among 255 x 200: 632 us by units, 84 in ranges).
 //  * Warps. Each unit goes to one warp, whose tiles are single chunks: the warps
 //    share nothing, and the four units of a CTA overlap. For many units of few
 //    tokens, which a CTA would start, join and end for too little (1024 requests of
-//    up to 100 tokens: 45.2 us, 84.1 with a CTA a unit; 512 of up to 250: 49.3 and
-//    57.2, in fp32 92 and 111; but 512 of up to 500: 90 and 87, and of up to 1000,
-//    d = 64: 95 and 87, as the warps that are left at the end load little). Where the
+//    up to 100 tokens: 47.0 us, 86.1 with a CTA a unit; 512 of up to 250: 50.0 and
+//    58.6, in fp32 93 and 111; but 512 of up to 500: 92 and 88, and of up to 1000,
+//    d = 64: 96 and 88, as the warps that are left at the end load little). Where the
 //    table could hold long requests and there are as many units, the split by ranges
 //    looks at the lengths and gives each warp the units that begin in its own equal
-//    range (1024 of up to 100: 57 us, 86 by CTAs' ranges; 512 of up to 130: 42 and 50;
-//    512 of up to 60 in fp32: 41 and 73; at the bound 800 of up to 250: 91 and 88, 512 of
-//    up to 250 with d = 64: 35 and 39).
+//    range (1024 of up to 100: 60 us, 90 by CTAs' ranges; 512 of up to 130: 45 and 53;
+//    512 of up to 60 in fp32: 41 and 75; at the bound 800 of up to 250: 96 and 94, 512 of
+//    up to 250 with d = 64: 37 and 41).
 // All work the bounds out on the device from lens, so a captured graph follows
 // the lengths.
 //
@@ -65,7 +65,7 @@ constexpr int kMaxCtas = 640;  // of the split by ranges (bounds the workspace)
 // What a unit costs a CTA beyond its tiles (Q, the join of the warps, the result),
 // in tiles. Ranges of equal tiles alone end far apart where short requests lie
 // together (256 requests of up to 500 tokens in a wide table: 66 us; with a cost of
-// 1, 2, 3 tiles a unit 55.7, 54.5, 55.2; 8 of up to 2500: 18.6; 18.0, 17.4, 17.3).
+// 1, 2, 3 tiles a unit 57.6, 55.3, 55.9; 8 of up to 2500: 18.6; 18.0, 17.6, 17.1).
 constexpr int kUnitCost = 2;
 // By warps: no unit of more tokens than this, and so many units a CTA at least.
 constexpr int kAloneTokens = 288, kAloneWaves = 2;
@@ -151,7 +151,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // bf16 numbers, so V^T P^T is two products: with one, O of 64 requests of up to 8192
 // tokens is off by 0.0022 of it, with two by 0.0017, which is its rounding to bf16. The
 // second costs up to 16 heads a pass 0 to 4 %, 17 to 32 heads 8 to 17 % (16 requests of
-// up to 65536 tokens, 2 KV heads of 32: 119.6 us and 139.8).
+// up to 65536 tokens, 2 KV heads of 32: 119.6 us and 137).
 // A lane is (r, c) = (lane / 4, lane % 4): tokens r and r + 8 and heads 2c, 2c + 1 of
 // S^T, features r and r + 8 of every 16 of O^T.
 template <int kD, int NT>
@@ -225,7 +225,7 @@ struct CoreBf16 {
     q_at = smem_u32(q_shared) + lane % 8 * (kD * 2) + ((lane / 8 ^ lane % 8) << 4);
   }
   // For one warp by itself, whose Q, where kQShared, has a place of its own (1024
-  // requests of up to 100 tokens, 2 KV heads of 16: 24.7 us, 39.1 by CTAs).
+  // requests of up to 100 tokens, 2 KV heads of 16: 26.8 us, 41.1 by CTAs).
   __device__ __forceinline__ void settle_alone(const DecodeArgs& a, long long q_row, int heads,
                                                char* q_own) {
     if constexpr (kQShared) {
@@ -783,11 +783,11 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
 }
 
 // How the work is cut (see above). kByRangesOrWarps chooses on the device; it is a
-// kernel of its own since its size costs short calls 0.6 us (5 requests of up to 4001
-// tokens in fp32: 12.2 us, 11.5 without the walk by warps) and long ones of 8 fp32
-// heads a pass, or 32 in bf16, registers (200 of up to 4000 tokens, 8 of 64: 373 us and
-// 364; 800 of up to 4000, 32 of 128: 172.5 and 168.5; where the units are short, 512 of
-// up to 50, 8 of 64: 39 and 92).
+// kernel of its own since its size costs short calls 0.3 us (5 requests of up to 4001
+// tokens in fp32: 11.4 us, 11.1 without the walk by warps) and long ones of 8 fp32
+// heads a pass, or 32 in bf16, registers (200 of up to 4000 tokens, 8 KV heads of 8: 365
+// us and 362; 800 of up to 4000, one of 32: 194 and 190; where the units are short, 512
+// of up to 50, 8 of 8: 38 and 93).
 enum Way { kByRanges, kByRangesOrWarps, kByUnits, kByWarps };
 
 template <class Core, Way kWay>

@@ -515,7 +515,8 @@ size_t xattn_paged_decode_workspace_bytes(const xattn_paged* cache);
  *   O[i, h] = sum_t softmax_t(Q[i, h] . K_t / sqrt(d)) V_t,   t < lens[i],
  * K_t, V_t the rows of token t of request i and KV head h / (hq / hkv). The
  * newest token's own K and V have to be in the cache (xattn_paged_append
- * first). A request with lens[i] = 0 gets O = 0 and lse = -inf.
+ * first). A request with lens[i] = 0 gets O = 0 and lse = -inf, as does a query
+ * head whose logits are all -inf (finite values).
  *
  * Q: [nseq, hq, d] contiguous (a [nseq, hq, 1, d] tensor of the other calls);
  * O: out, like Q. lse: out, optional (may be NULL), fp32 [nseq, hq], the

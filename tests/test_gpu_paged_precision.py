@@ -142,6 +142,36 @@ def test_values_near_the_top_of_the_range(dtype, d, n, hkv, width):
     assert bool(((lse - math.log(79 + math.exp(key))).abs() <= 2.0 ** -16).all())
 
 
+@pytest.mark.parametrize("lens,hkv,width", [([1, 17, 300, 2000], 2, 0), ([1, 17, 300, 2000], 2, 900),
+                                            ([90] * 140, 8, 0), ([90] * 140, 8, 600)])
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_logits_that_are_all_minus_infinity(dtype, d, lens, hkv, width):
+    """The second query head of each group of three sees no key at all; its neighbours do."""
+    table, N = _table(lens, 16, width=width)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    kp, vp = (torch.randn(N, hkv, 16, d, device=DEV, generator=g).to(dtype) for _ in range(2))
+    kp[..., 1] = -math.inf
+    Q = torch.randn(len(lens), 3 * hkv, d, device=DEV, generator=g).to(dtype)
+    Q[..., 1] = 0.0
+    got, lse = _decode(Q, kp, vp, table, _i32(lens))
+    assert bool(got.isnan().all()) and bool(lse.isnan().all())      # 0 times an infinity
+    kp[..., 1] = torch.finfo(dtype).min
+    Q[:, 1::3, 1] = torch.finfo(dtype).max                          # a logit past fp32's range
+    got, lse = _decode(Q, kp, vp, table, _i32(lens))
+    sees = torch.arange(3 * hkv, device=DEV) % 3 != 1
+    assert bool((got[:, ~sees] == 0).all()) and bool((lse[:, ~sees] == -math.inf).all())
+    L = _i32(lens)
+    O, want, A, size_s = _exact(Q[:, sees], kp, vp, table, L)
+    half = R.BF16_HALF if dtype == BF else R.F32_HALF
+    weight = 2.0 ** -16 if dtype == BF else 0.0      # the bounds of the first test
+    ds = (d + 6) * 2.0 ** -23 * size_s
+    sums = (L.double()[:, None] + 64) * 2.0 ** -23
+    tol = A * (weight + 2 * ds + sums + 2.0 ** -20)[..., None]
+    tol += half * (O.abs() + tol) + 1e-30
+    assert bool(((got[:, sees] - O).abs() <= tol).all())
+    assert bool(((lse[:, sees] - want).abs() <= ds + sums + 2.0 ** -20 + 2.0 ** -22 * want.abs()).all())
+
+
 def _marked_pages(N, hkv, page, d, dtype, seed):
     """Values that mark their token's place: piece p of 8 tokens of the pool has a 1 in feature
     p % d and zeros elsewhere. With equal weights O then counts a request's pieces by feature."""
