@@ -325,9 +325,10 @@ struct CoreBf16 {
       l[t][1] += w[1] + w[3];
       // The tensor cores take bf16: a weight goes to them cut to 8 bits, and what
       // that leaves, rounded, as a second term; together off by 2^-16 of it at
-      // most. The sum keeps the fp32 one. The second term is above zero (2^-17 of
-      // the weight where nothing is left), so that a value of infinity stays one:
-      // times 0 or times a negative term it would make a NaN.
+      // most. The sum keeps the fp32 one. The second term of a weight above zero is
+      // above zero (where nothing is left 2^-17 of it and the smallest weight, 2^-126),
+      // so that a value of infinity stays one: times 0 or times a negative term it
+      // would make a NaN.
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float low[2];
@@ -335,7 +336,7 @@ struct CoreBf16 {
         for (int y = 0; y < 2; ++y) {
           const float u = w[2 * x + y];
           const float cut = __uint_as_float(__float_as_uint(u) & 0xffff0000u);
-          low[y] = fmaxf(u - cut, u * 0x1p-17f);
+          low[y] = fmaxf(u - cut, fminf(u, fmaf(u, 0x1p-17f, 0x1p-126f)));
         }
         p[t][x] = transpose8x8(
             __byte_perm(__float_as_uint(w[2 * x]), __float_as_uint(w[2 * x + 1]), 0x7632));

@@ -47,9 +47,8 @@ def decode_buffers(Q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor) 
 def _aligned(*tensors: torch.Tensor) -> None:
     """The library refuses a tensor that does not start on a 16-byte boundary; here it has
     to be known before the plan is made."""
-    for t in tensors:
-        if t.data_ptr() % 16:
-            raise ValueError("a tensor does not start on a 16-byte boundary")
+    if any(t.data_ptr() % 16 for t in tensors):
+        raise ValueError("a tensor does not start on a 16-byte boundary")
 
 
 class PagedCache:
@@ -76,6 +75,7 @@ class PagedCache:
         self.lens = torch.zeros(nseq, **i32)
         self.ring = torch.arange(num_pages, **i32)
         self.pool = torch.tensor([0, num_pages], **i32)
+        self._ws_bytes = {}     # of the decode, by query heads (the rest of its shape is fixed)
 
     def plan(self, fresh: torch.Tensor, buffers: dict):
         """Pages and slots for ``fresh[i]`` new tokens of request i (-1 ends
@@ -134,8 +134,11 @@ class PagedCache:
                                and K.stride(0) * K.element_size() % 16 == 0):
             raise ValueError("the tokens of K and V must not overlap and lie a multiple of 16 "
                              "bytes apart")
-        need = xattn_paged_decode_workspace_bytes(
-            make_paged(self.k_pages, Q.shape[1], Q.shape[0], self.table.shape[1]))
+        hq = Q.shape[1]
+        need = self._ws_bytes.get(hq)
+        if need is None:
+            need = self._ws_bytes[hq] = xattn_paged_decode_workspace_bytes(
+                make_paged(self.k_pages, hq, Q.shape[0], self.table.shape[1]))
         if need == 0 or ws.nbytes < need:
             raise ValueError("the heads do not fit the cache, or the workspace is too small")
         self.plan(fresh, buffers)

@@ -172,6 +172,31 @@ def test_logits_that_are_all_minus_infinity(dtype, d, lens, hkv, width):
     assert bool(((lse[:, sees] - want).abs() <= ds + sums + 2.0 ** -20 + 2.0 ** -22 * want.abs()).all())
 
 
+@pytest.mark.parametrize("n,hkv,width", [(2, 2, 0), (2, 2, 2000), (140, 8, 0), (140, 8, 600)])
+@pytest.mark.parametrize("group", [3, 12, 32])
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_infinite_values_of_tokens_that_weigh_next_to_nothing(dtype, d, group, n, hkv, width):
+    """Token t's value is infinite in feature t and its weight falls from 1 to e^-80 or so,
+    which fp32 holds: O is infinite there, with the value's sign, and finite elsewhere."""
+    T = d // 2
+    table, N = _table([T + 3] * n, 16, width=width)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    kp, vp = torch.zeros(N, hkv, 16, d, device=DEV, dtype=dtype), \
+        torch.randn(N, hkv, 16, d, device=DEV, generator=g).to(dtype)
+    t = torch.arange(T, device=DEV)
+    sign = torch.where(t % 3 == 1, -1.0, 1.0).to(dtype)
+    for i in range(n):
+        at = table[i].long()[t // 16]
+        kp[at, :, t % 16, 3] = (-(78.0 / T) * math.sqrt(d) * t)[:, None].to(dtype)
+        vp[at, :, t % 16, t] = (sign * math.inf)[:, None]
+    Q = torch.zeros(n, group * hkv, d, device=DEV, dtype=dtype)
+    kp[..., 5] = torch.randn(N, hkv, 16, device=DEV, generator=g).to(dtype)
+    Q[..., 3], Q[..., 5] = 1.0, torch.rand(n, group * hkv, device=DEV, generator=g).to(dtype)
+    got, lse = _decode(Q, kp, vp, table, _i32([T + 3] * n))
+    assert bool((got[..., :T] == sign.double() * math.inf).all())
+    assert bool(got[..., T:].isfinite().all()) and bool(lse.isfinite().all())
+
+
 def _marked_pages(N, hkv, page, d, dtype, seed):
     """Values that mark their token's place: piece p of 8 tokens of the pool has a 1 in feature
     p % d and zeros elsewhere. With equal weights O then counts a request's pieces by feature."""
