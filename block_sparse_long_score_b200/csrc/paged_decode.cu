@@ -151,7 +151,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // bf16 numbers, so V^T P^T is two products: with one, O of 64 requests of up to 8192
 // tokens is off by 0.0022 of it, with two by 0.0017, which is its rounding to bf16. The
 // second costs up to 16 heads a pass 0 to 4 %, 17 to 32 heads 8 to 17 % (16 requests of
-// up to 65536 tokens, 2 KV heads of 32: 119.6 us and 137).
+// up to 65536 tokens, 2 KV heads of 32: 119.6 us and 139).
 // A lane is (r, c) = (lane / 4, lane % 4): tokens r and r + 8 and heads 2c, 2c + 1 of
 // S^T, features r and r + 8 of every 16 of O^T.
 template <int kD, int NT>
@@ -784,11 +784,10 @@ __device__ void empty_rows(const DecodeArgs& a, int group, int groups, int part,
 }
 
 // How the work is cut (see above). kByRangesOrWarps chooses on the device; it is a
-// kernel of its own since its size costs short calls 0.3 us (5 requests of up to 4001
-// tokens in fp32: 11.4 us, 11.1 without the walk by warps) and long ones of 8 fp32
-// heads a pass, or 32 in bf16, registers (200 of up to 4000 tokens, 8 KV heads of 8: 365
-// us and 362; 800 of up to 4000, one of 32: 194 and 190; where the units are short, 512
-// of up to 50, 8 of 8: 38 and 93).
+// kernel of its own since its size costs long units of 8 fp32 heads a pass, or 32 in
+// bf16, registers (200 of up to 4000 tokens, 8 KV heads of 8: 362 us, 360 without the walk
+// by warps; 800 of up to 4000, one of 32: 197 and 193; where the units are short, 512 of
+// up to 50, 8 of 8: 38 and 93).
 enum Way { kByRanges, kByRangesOrWarps, kByUnits, kByWarps };
 
 template <class Core, Way kWay>
