@@ -295,10 +295,10 @@ struct CoreBf16 {
     }
     // The reference m that a weight is taken against is set to kLead above the
     // maximum so far, and set again (o and l are rescaled) only when a logit passes
-    // it, which after a few chunks hardly happens. So no weight is above 1, the
-    // largest is 2^-kLead at least, and values up to the top of fp32 times a few
-    // such weights stay finite before the division; fp32 holds weights down to
-    // 2^-118 of the largest, and their rounding is relative.
+    // it, which after a few chunks hardly happens. So no weight is above the one
+    // against the maximum itself, 1 at most, and products with large values overflow
+    // no earlier than with those; the largest is 2^-kLead at least, fp32 holds weights
+    // down to 2^-118 of it, and their rounding is relative.
     bool grow = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
